@@ -273,6 +273,150 @@ HSTU_API hstu_status_t hstu_cand_fwd(const hstu_problem_t *p, const void *k_hist
                                      const void *v, const void *u, void *y, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/*
+ * Rows ahead of a layer's projection: the root-mean-square norm of the layer
+ * input with the residual's addition, and 8-bit rows (the reproduction note's
+ * U, V, Q, K = Split(SiLU(Norm(X) W_UVQK)) names the norm).
+ *
+ *   h_te = round(x_te + residual_te)          (x itself without a residual)
+ *   r_t  = 1 / sqrt(mean_e h_te^2 + eps),     v_te = h_te r_t weight_e
+ *   y    = round(v)     and / or     q8 = e4m3(v / s_t),  s_t = max(max_e |v_te|, 2^-100) / 448
+ *
+ * x, residual, h, y [T, E] in dtype; weight fp32 [E] or NULL (ones); q8 [T, E]
+ * e4m3 bytes with q8_scale fp32 [T] (both or neither); rstd fp32 [T] or NULL.
+ * At least one of y and q8 is required.  h may be NULL, and is only written
+ * with a residual; it may be x or residual, and y may be any of the three.
+ * Sums are fp32 (a row whose sum of squares exceeds fp32 gives zeros); a row
+ * that holds a NaN gives NaN.  Any E from 1 to 16384 and any alignment of
+ * whole elements; E a multiple of 16 bytes with 16-byte aligned pointers (the
+ * bytes of q8: 8 with bf16, 4 with fp32) takes the vector path.  No workspace.
+ */
+HSTU_API hstu_status_t hstu_rmsnorm_fwd(hstu_dtype_t dtype, int32_t T, int32_t E, const void *x,
+                                        const void *residual, const float *weight, float eps,
+                                        void *h, void *y, uint8_t *q8, float *q8_scale,
+                                        float *rstd, void *stream);
+
+/* Rows as they are in 8 bits: q8 = e4m3(x / s_t), s_t = max(max_e |x_te|, 2^-100) / 448
+ * (hstu_uvqk_fp8_fwd's weights are rows too).  E from 1 to 16384. */
+HSTU_API hstu_status_t hstu_quant_rows(hstu_dtype_t dtype, int32_t T, int32_t E, const void *x,
+                                       uint8_t *q8, float *q8_scale, void *stream);
+
+/*
+ * Backward of the norm, from dy [T, E], the forward's h (x without a residual)
+ * and rstd:
+ *   g = weight dy,   dx = d_residual + r (g - h r^2 mean_e(g h)),
+ *   d_weight_e = sum_t dy_te h_te r_t
+ * dx is the gradient of x and of the residual alike; d_residual [T, E] or NULL
+ * is the gradient that reaches h by the residual stream; dx may be d_residual
+ * or dy.  d_weight fp32 [E] or NULL is overwritten, and added up in an order
+ * that depends on the sizes alone.  With d_weight, workspace:
+ * hstu_rmsnorm_bwd_workspace_size bytes, 256-byte aligned, any contents (it
+ * holds no status word).
+ */
+HSTU_API size_t hstu_rmsnorm_bwd_workspace_size(int32_t T, int32_t E);
+HSTU_API hstu_status_t hstu_rmsnorm_bwd(hstu_dtype_t dtype, int32_t T, int32_t E, const void *dy,
+                                        const void *h, const float *rstd, const float *weight,
+                                        const void *d_residual, void *dx, float *d_weight,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * UVQK projection of 8-bit rows: act((x8 w8^T) x_scale_t w_scale_n + bias_n),
+ * split and laid out as by hstu_uvqk_fwd (bf16 outputs, rounded once).
+ * x8 [T, E], w8 [N, E] e4m3; x_scale fp32 [T], w_scale fp32 [N]; all pointers
+ * 16-byte aligned.  Supported: E a multiple of 16; H*d_v and H*d_qk multiples
+ * of 256; T <= 8388480.  workspace: 256 bytes, as for hstu_uvqk_fwd.
+ */
+HSTU_API hstu_status_t hstu_uvqk_fp8_fwd(int32_t T, int32_t E, int32_t H, int32_t d_qk,
+                                         int32_t d_v, int32_t act, const uint8_t *x8,
+                                         const float *x_scale, const uint8_t *w8,
+                                         const float *w_scale, const float *bias, void *u, void *v,
+                                         void *q, void *k, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
+/*
+ * The position-bias table of the attention from learned buckets, and its
+ * gradient: for distances d = i - j in [0, L)
+ *   rab_pos[h][L-1+d] = table[h][bucket(d)]        (0 for d < 0)
+ *   d_table[h][k]     = sum_{d: bucket(d) = k} d_rab_pos[h][L-1+d]
+ * bucket(d) = number of thresholds <= d.  thresholds: HOST memory, int32
+ * [num_buckets - 1], ascending (equal neighbours leave a bucket empty), each
+ * >= 1; read during the call.  num_buckets in [1, 128]; L >= 1; H <= 65535.
+ * Entries d < 0 of d_rab_pos are not read.  The gradient is added up in a
+ * fixed order.  Both outputs are overwritten.  No workspace.
+ */
+HSTU_API hstu_status_t hstu_rab_bucket_fwd(int32_t H, int32_t L, int32_t num_buckets,
+                                           const int32_t *thresholds, const float *table,
+                                           float *rab_pos, void *stream);
+HSTU_API hstu_status_t hstu_rab_bucket_bwd(int32_t H, int32_t L, int32_t num_buckets,
+                                           const int32_t *thresholds, const float *d_rab_pos,
+                                           float *d_table, void *stream);
+
+/*
+ * Host utility: thresholds of buckets that are exact up to max_exact and then
+ * logarithmic up to max_distance:
+ *   bucket(d) = d                                            for d < max_exact
+ *             = min(NB - 1, max_exact + floor((NB - max_exact)
+ *                   ln(d / max_exact) / ln(max_distance / max_exact)))  otherwise
+ * found in whole numbers.  Writes out[0 .. NB-2]; returns the number written,
+ * or -1 for num_buckets outside [1, 128], max_exact outside [1, num_buckets]
+ * or max_distance <= max_exact where a logarithmic bucket exists.
+ */
+HSTU_API int32_t hstu_pos_bucket_thresholds(int32_t *out, int32_t num_buckets, int32_t max_exact,
+                                            int32_t max_distance);
+
+/*
+ * Keys and values of cached histories in 4 bits.  Each head's 128 values of a
+ * token are four groups of 32 with one scale s each, the smallest number of
+ * five significant bits at or above max|x| / 7 (max|x| taken as at least
+ * 2^-100), and whole numbers n = rint(x / s) in -7..7 (ties to even); what the
+ * cache holds is n s, a bf16 number.  A group with an infinity or NaN reads as
+ * NaN.
+ *   codes  [cache_rows, H, 64] bytes: a little-endian 32-bit word holds eight
+ *          values, value 2i in bits 4i.., value 2i+1 in bits 16+4i.., as n + 8
+ *   scales [cache_rows, H, 4] bf16
+ * hstu_kv4_pack writes T tokens of k, v [T, H, 128] bf16 to the cache rows
+ * rows[t] (device int32 [T], distinct, -1: the token is skipped), or to rows
+ * 0..T-1 when rows is NULL; other rows stay as they are.  hstu_kv4_unpack
+ * reads rows back (a token of row -1 keeps its k, v).  Rows outside
+ * [-1, cache_rows) are skipped and reported by hstu_attn_check.  All pointers
+ * 16-byte aligned (rows: 4).  workspace: 256 bytes with the status word.
+ */
+HSTU_API hstu_status_t hstu_kv4_pack(int32_t T, int32_t H, const void *k, const void *v,
+                                     const int32_t *rows, int32_t cache_rows, void *k_codes,
+                                     void *k_scales, void *v_codes, void *v_scales,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+HSTU_API hstu_status_t hstu_kv4_unpack(int32_t T, int32_t H, const void *k_codes,
+                                       const void *k_scales, const void *v_codes,
+                                       const void *v_scales, const int32_t *rows,
+                                       int32_t cache_rows, void *k, void *v, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/*
+ * hstu_cand_fwd against histories in a 4-bit cache.  Everything but the
+ * history's keys and values is as there; user b's history is the cache rows
+ * first_rows[b] .. first_rows[b] + n_b - 1 (device int32 [B]; NULL: the rows
+ * are packed as the tokens are, first row offsets[b], cache_rows >=
+ * total_tokens).  Users may share rows.  timestamps stay packed by offsets.
+ * p->total_tokens need only bound offsets[B] (and the timestamps' length).
+ * Supported: bf16, d_qk = d_v = 128, 1 <= H <= 16.  Groups whose scale exceeds
+ * 2^123 are not finite here.  workspace: hstu_cand_kv4_workspace_size bytes,
+ * 256-byte aligned, zero-filled before its first use; beyond the status word
+ * it keeps nothing from one call to the next, so calls of different sizes may
+ * use it one after another.  The size grows with every argument but num_heads:
+ * a workspace serves every call of as many heads with no larger sizes.
+ */
+HSTU_API size_t hstu_cand_kv4_workspace_size(int32_t batch, int32_t num_heads,
+                                             int32_t max_seq_len, int32_t total_cands,
+                                             int32_t max_cands);
+HSTU_API hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t *p, const void *k_codes,
+                                         const void *k_scales, const void *v_codes,
+                                         const void *v_scales, int32_t cache_rows,
+                                         const int32_t *first_rows, const int32_t *cand_offsets,
+                                         int32_t total_cands, int32_t max_cands,
+                                         const int64_t *cand_timestamps, const void *q,
+                                         const void *k, const void *v, const void *u, void *y,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,11 @@ HSTU_F32, HSTU_BF16 = 0, 1
 EXPORTED = ("hstu_attn_workspace_size", "hstu_attn_fwd", "hstu_attn_bwd", "hstu_attn_check",
             "hstu_status_string", "hstu_time_bucket_thresholds", "hstu_selftest_wait_timeout",
             "hstu_attn_bwd_noalloc", "hstu_uvqk_fwd", "hstu_out_fwd", "hstu_cand_workspace_size",
-            "hstu_cand_fwd")
+            "hstu_cand_fwd", "hstu_rmsnorm_fwd", "hstu_rmsnorm_bwd",
+            "hstu_rmsnorm_bwd_workspace_size", "hstu_quant_rows", "hstu_uvqk_fp8_fwd",
+            "hstu_rab_bucket_fwd", "hstu_rab_bucket_bwd", "hstu_pos_bucket_thresholds",
+            "hstu_kv4_pack", "hstu_kv4_unpack", "hstu_cand_kv4_workspace_size",
+            "hstu_cand_kv4_fwd")
 
 
 class HSTUError(RuntimeError):
@@ -98,6 +102,30 @@ def load_library():
     lib.hstu_cand_workspace_size.restype = sz
     lib.hstu_cand_fwd.argtypes = [P, vp, vp, vp, i32, i32] + [vp] * 6 + [vp, sz, vp]
     lib.hstu_cand_fwd.restype = ctypes.c_int
+    f32, it = ctypes.c_float, ctypes.c_int
+    lib.hstu_rmsnorm_fwd.argtypes = [it, i32, i32, vp, vp, vp, f32] + [vp] * 6
+    lib.hstu_rmsnorm_fwd.restype = it
+    lib.hstu_quant_rows.argtypes = [it, i32, i32] + [vp] * 4
+    lib.hstu_quant_rows.restype = it
+    lib.hstu_rmsnorm_bwd_workspace_size.argtypes = [i32, i32]
+    lib.hstu_rmsnorm_bwd_workspace_size.restype = sz
+    lib.hstu_rmsnorm_bwd.argtypes = [it, i32, i32] + [vp] * 8 + [sz, vp]
+    lib.hstu_rmsnorm_bwd.restype = it
+    lib.hstu_uvqk_fp8_fwd.argtypes = [i32] * 6 + [vp] * 10 + [sz, vp]
+    lib.hstu_uvqk_fp8_fwd.restype = it
+    for f in (lib.hstu_rab_bucket_fwd, lib.hstu_rab_bucket_bwd):
+        f.argtypes = [i32, i32, i32] + [vp] * 4
+        f.restype = it
+    lib.hstu_pos_bucket_thresholds.argtypes = [vp, i32, i32, i32]
+    lib.hstu_pos_bucket_thresholds.restype = i32
+    lib.hstu_kv4_pack.argtypes = [i32, i32, vp, vp, vp, i32] + [vp] * 5 + [sz, vp]
+    lib.hstu_kv4_pack.restype = it
+    lib.hstu_kv4_unpack.argtypes = [i32, i32] + [vp] * 5 + [i32] + [vp] * 3 + [sz, vp]
+    lib.hstu_kv4_unpack.restype = it
+    lib.hstu_cand_kv4_workspace_size.argtypes = [i32] * 5
+    lib.hstu_cand_kv4_workspace_size.restype = sz
+    lib.hstu_cand_kv4_fwd.argtypes = [P] + [vp] * 4 + [i32, vp, vp, i32, i32] + [vp] * 7 + [sz, vp]
+    lib.hstu_cand_kv4_fwd.restype = it
     _lib = lib
     return lib
 
@@ -373,4 +401,383 @@ def hstu_cand_fwd(k_hist, v_hist, offsets, max_seq_len, q, k, v, u, cand_offsets
                            _stream_ptr(stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_cand_fwd")
+    return y
+
+
+def _rows_dtype(t):
+    if t.dtype == torch.bfloat16:
+        return HSTU_BF16
+    if t.dtype == torch.float32:
+        return HSTU_F32
+    raise ValueError("rows must be bf16 or fp32")
+
+
+def _shape(t, name, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+def _on(ref, *tensors):
+    """A context in which ref's device is current; every tensor must be there."""
+    for t in tensors:
+        if t is not None and t.device != ref.device:
+            raise ValueError("all tensors must be on one device (%s and %s)" % (ref.device, t.device))
+    return torch.cuda.device(ref.device)
+
+
+def hstu_rmsnorm_fwd(x, *, residual=None, weight=None, eps: float = 1e-6, quant: bool = False,
+                     save_rstd: bool = False, out=None, stream=None):
+    """Root-mean-square norm of the rows of x + residual (x [T, E], bf16 or fp32).
+
+    Returns a dict: h = round(x + residual) (None without a residual); y, or with
+    quant q8 (e4m3) and scale (fp32 [T]); rstd (fp32 [T], None unless save_rstd).
+    ``out`` may hold any of these tensors to write to."""
+    lib = load_library()
+    _dev(x, "x")
+    dt = _rows_dtype(x)
+    _dev(residual, "residual", x.dtype)
+    _dev(weight, "weight", torch.float32)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, E]")
+    T, E = x.shape
+    _shape(residual, "residual", T, E)
+    _shape(weight, "weight", E)
+    res = dict(h=None, y=None, q8=None, scale=None, rstd=None)
+    res.update(out or {})
+    with _on(x, residual, weight, *res.values()):
+        if residual is not None and res["h"] is None:
+            res["h"] = torch.empty_like(x)
+        if quant:
+            if res["q8"] is None:
+                res["q8"] = torch.empty((T, E), dtype=torch.float8_e4m3fn, device=x.device)
+            if res["scale"] is None:
+                res["scale"] = torch.empty(T, dtype=torch.float32, device=x.device)
+        elif res["y"] is None:
+            res["y"] = torch.empty_like(x)
+        if save_rstd and res["rstd"] is None:
+            res["rstd"] = torch.empty(T, dtype=torch.float32, device=x.device)
+        for n, t, shape in (("h", x.dtype, (T, E)), ("y", x.dtype, (T, E)),
+                            ("q8", torch.float8_e4m3fn, (T, E)), ("scale", torch.float32, (T,)),
+                            ("rstd", torch.float32, (T,))):
+            _dev(res[n], n, t)
+            _shape(res[n], n, *shape)
+        rc = lib.hstu_rmsnorm_fwd(dt, T, E, _ptr(x), _ptr(residual), _ptr(weight), float(eps),
+                                  _ptr(res["h"]), _ptr(res["y"]), _ptr(res["q8"]),
+                                  _ptr(res["scale"]), _ptr(res["rstd"]), _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_rmsnorm_fwd")
+    return res
+
+
+def hstu_rmsnorm_bwd(dy, h, rstd, *, weight=None, d_residual=None, need_weight_grad=True,
+                     dx=None, workspace=None, stream=None):
+    """Backward of hstu_rmsnorm_fwd from its h (x without a residual) and rstd.
+    Returns (dx, d_weight fp32 [E] or None); dx is the residual's gradient too."""
+    lib = load_library()
+    _dev(dy, "dy")
+    dt = _rows_dtype(dy)
+    _dev(h, "h", dy.dtype)
+    _dev(rstd, "rstd", torch.float32)
+    _dev(weight, "weight", torch.float32)
+    _dev(d_residual, "d_residual", dy.dtype)
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, E]")
+    T, E = dy.shape
+    _shape(h, "h", T, E)
+    _shape(rstd, "rstd", T)
+    _shape(weight, "weight", E)
+    _shape(d_residual, "d_residual", T, E)
+    with _on(dy, h, rstd, weight, d_residual, dx, workspace):
+        if dx is None:
+            dx = torch.empty_like(dy)
+        _dev(dx, "dx", dy.dtype)
+        _shape(dx, "dx", T, E)
+        dw = torch.empty(E, dtype=torch.float32, device=dy.device) if need_weight_grad else None
+        if need_weight_grad and workspace is None:
+            workspace = torch.empty(int(lib.hstu_rmsnorm_bwd_workspace_size(T, E)),
+                                    dtype=torch.uint8, device=dy.device)
+        rc = lib.hstu_rmsnorm_bwd(dt, T, E, _ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight),
+                                  _ptr(d_residual), _ptr(dx), _ptr(dw), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(),
+                                  _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_rmsnorm_bwd")
+    return dx, dw
+
+
+def hstu_quant_rows(x, *, stream=None):
+    """Rows of x [T, E] (bf16 or fp32) as e4m3 bytes with one scale each.
+    Returns (q8 [T, E] float8_e4m3fn, scale fp32 [T])."""
+    lib = load_library()
+    _dev(x, "x")
+    dt = _rows_dtype(x)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, E]")
+    T, E = x.shape
+    with _on(x):
+        q8 = torch.empty((T, E), dtype=torch.float8_e4m3fn, device=x.device)
+        scale = torch.empty(T, dtype=torch.float32, device=x.device)
+        rc = lib.hstu_quant_rows(dt, T, E, _ptr(x), _ptr(q8), _ptr(scale), _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_quant_rows")
+    return q8, scale
+
+
+def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: int, *, bias=None,
+                      act: int = 0, out=None, workspace=None, stream=None):
+    """UVQK projection act(x w^T + bias) of 8-bit rows: x8 [T, E], w8 [N, E]
+    (float8_e4m3fn) with fp32 scales per row.  Returns the dict of hstu_uvqk_fwd."""
+    lib = load_library()
+    for n, t in (("x8", x8), ("w8", w8)):
+        _dev(t, n, torch.float8_e4m3fn)
+    for n, t in (("x_scale", x_scale), ("w_scale", w_scale), ("bias", bias)):
+        _dev(t, n, torch.float32)
+    T, E = x8.shape
+    H = int(num_heads)
+    N = 2 * H * (int(d_qk) + int(d_v))
+    _shape(w8, "w8", N, E)
+    _shape(x_scale, "x_scale", T)
+    _shape(w_scale, "w_scale", N)
+    _shape(bias, "bias", N)
+    with _on(x8, x_scale, w8, w_scale, bias, workspace, *(out or {}).values()):
+        if out is None:
+            kw = dict(dtype=torch.bfloat16, device=x8.device)
+            out = dict(u=torch.empty((T, H * d_v), **kw), v=torch.empty((T, H, d_v), **kw),
+                       q=torch.empty((T, H, d_qk), **kw), k=torch.empty((T, H, d_qk), **kw))
+        for n, shape in (("u", (T, H * d_v)), ("v", (T, H, d_v)), ("q", (T, H, d_qk)),
+                         ("k", (T, H, d_qk))):
+            _dev(out[n], n, torch.bfloat16)
+            _shape(out[n], n, *shape)
+        if workspace is None:
+            workspace = _status_workspace(x8.device)
+        rc = lib.hstu_uvqk_fp8_fwd(T, E, H, int(d_qk), int(d_v), int(act), _ptr(x8),
+                                   _ptr(x_scale), _ptr(w8), _ptr(w_scale), _ptr(bias),
+                                   _ptr(out["u"]), _ptr(out["v"]), _ptr(out["q"]), _ptr(out["k"]),
+                                   _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_uvqk_fp8_fwd")
+    return out
+
+
+def hstu_pos_bucket_thresholds(num_buckets: int, max_exact: int, max_distance: int):
+    """int32 CPU tensor [num_buckets - 1]: the smallest distance of each bucket
+    from 1 on, exact up to max_exact, then logarithmic up to max_distance."""
+    out = torch.zeros(max(int(num_buckets) - 1, 1), dtype=torch.int32)
+    n = load_library().hstu_pos_bucket_thresholds(
+        _ptr(out) if 1 <= num_buckets <= 128 else None, int(num_buckets), int(max_exact),
+        int(max_distance))
+    if n < 0:
+        raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_pos_bucket_thresholds")
+    return out[:n]
+
+
+def _thresholds(thr, nb):
+    if not isinstance(thr, torch.Tensor) or thr.device.type != "cpu" or thr.dtype != torch.int32:
+        raise ValueError("thresholds must be an int32 CPU tensor")
+    thr = thr.contiguous()
+    _shape(thr, "thresholds", nb - 1)
+    return thr
+
+
+def hstu_rab_bucket_fwd(table, length: int, thresholds, *, out=None, stream=None):
+    """Position-bias table rab_pos [H, 2 length - 1] (fp32) from table [H, NB] and
+    the buckets' thresholds (int32 CPU tensor [NB - 1])."""
+    lib = load_library()
+    _dev(table, "table", torch.float32)
+    H, NB = table.shape
+    thr = _thresholds(thresholds, NB)
+    length = int(length)
+    if length < 1:
+        raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_rab_bucket_fwd")
+    with _on(table, out):
+        if out is None:
+            out = torch.empty((H, 2 * length - 1), dtype=torch.float32, device=table.device)
+        _dev(out, "out", torch.float32)
+        _shape(out, "out", H, 2 * length - 1)
+        rc = lib.hstu_rab_bucket_fwd(H, length, NB, _ptr(thr), _ptr(table), _ptr(out),
+                                     _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_rab_bucket_fwd")
+    return out
+
+
+def hstu_rab_bucket_bwd(d_rab_pos, num_buckets: int, thresholds, *, out=None, stream=None):
+    """Gradient [H, num_buckets] of hstu_rab_bucket_fwd's table from that of
+    rab_pos [H, 2L - 1] (hstu_attn_bwd's d_rab_pos)."""
+    lib = load_library()
+    _dev(d_rab_pos, "d_rab_pos", torch.float32)
+    H, W = d_rab_pos.shape
+    if W % 2 != 1:
+        raise ValueError("d_rab_pos must be [H, 2L - 1]")
+    NB = int(num_buckets)
+    thr = _thresholds(thresholds, NB)
+    with _on(d_rab_pos, out):
+        if out is None:
+            out = torch.empty((H, NB), dtype=torch.float32, device=d_rab_pos.device)
+        _dev(out, "out", torch.float32)
+        _shape(out, "out", H, NB)
+        rc = lib.hstu_rab_bucket_bwd(H, (W + 1) // 2, NB, _ptr(thr), _ptr(d_rab_pos), _ptr(out),
+                                     _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_rab_bucket_bwd")
+    return out
+
+
+def hstu_kv4_cache(cache_rows: int, num_heads: int, device):
+    """An empty 4-bit cache: (k_codes, k_scales, v_codes, v_scales), codes uint8
+    [cache_rows, H, 64], scales bf16 [cache_rows, H, 4]; it reads as zeros."""
+    R, H = int(cache_rows), int(num_heads)
+    codes = lambda: torch.full((R, H, 64), 0x88, dtype=torch.uint8, device=device)
+    scales = lambda: torch.zeros((R, H, 4), dtype=torch.bfloat16, device=device)
+    return codes(), scales(), codes(), scales()
+
+
+def _check_cache(cache):
+    kc, ks, vc, vs = cache
+    for n, t in (("k_codes", kc), ("v_codes", vc)):
+        _dev(t, n, torch.uint8)
+    for n, t in (("k_scales", ks), ("v_scales", vs)):
+        _dev(t, n, torch.bfloat16)
+    R, H = kc.shape[0], kc.shape[1]
+    for n, t, w in (("k_codes", kc, 64), ("k_scales", ks, 4), ("v_codes", vc, 64),
+                    ("v_scales", vs, 4)):
+        _shape(t, n, R, H, w)
+    return R, H
+
+
+def hstu_kv4_pack(k, v, *, cache=None, rows=None, workspace=None, stream=None):
+    """Writes keys and values [T, H, 128] (bf16) to a 4-bit cache: to the rows
+    ``rows`` (int32 [T], distinct, -1 skips), else to rows 0..T-1.  Without
+    ``cache`` a new one of T rows.  Returns the cache."""
+    lib = load_library()
+    for n, t in (("k", k), ("v", v)):
+        _dev(t, n, torch.bfloat16)
+    _dev(rows, "rows", torch.int32)
+    T, H = k.shape[0], k.shape[1]
+    for n, t in (("k", k), ("v", v)):
+        _shape(t, n, T, H, 128)
+    _shape(rows, "rows", T)
+    with _on(k, v, rows, workspace, *(cache or ())):
+        if cache is None:
+            if rows is not None:
+                raise ValueError("rows need a cache")
+            kw = dict(device=k.device)
+            cache = tuple(torch.empty((T, H, w), dtype=dt, **kw)
+                          for w, dt in ((64, torch.uint8), (4, torch.bfloat16)) * 2)
+        R, HC = _check_cache(cache)
+        if HC != H:
+            raise ValueError("the cache has %d heads, k has %d" % (HC, H))
+        if workspace is None:
+            workspace = _status_workspace(k.device)
+        rc = lib.hstu_kv4_pack(T, H, _ptr(k), _ptr(v), _ptr(rows), R, *[_ptr(t) for t in cache],
+                               _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_kv4_pack")
+    return cache
+
+
+def hstu_kv4_unpack(cache, *, rows=None, out=None, workspace=None, stream=None):
+    """Keys and values [T, H, 128] (bf16) of a 4-bit cache's rows ``rows``
+    (int32 [T]; a token of row -1 keeps what ``out`` holds), else of all rows."""
+    lib = load_library()
+    _dev(rows, "rows", torch.int32)
+    R, H = _check_cache(cache)
+    T = R if rows is None else rows.numel()
+    with _on(cache[0], *cache, rows, workspace, *(out or ())):
+        if out is None:
+            new = torch.empty if rows is None else torch.zeros
+            out = tuple(new((T, H, 128), dtype=torch.bfloat16, device=cache[0].device)
+                        for _ in range(2))
+        k, v = out
+        for n, t in (("k", k), ("v", v)):
+            _dev(t, n, torch.bfloat16)
+            _shape(t, n, T, H, 128)
+        if workspace is None:
+            workspace = _status_workspace(k.device)
+        rc = lib.hstu_kv4_unpack(T, H, *[_ptr(t) for t in cache], _ptr(rows), R, _ptr(k), _ptr(v),
+                                 _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_kv4_unpack")
+    return k, v
+
+
+def hstu_cand_kv4_workspace(batch: int, num_heads: int, max_seq_len: int, total_cands: int,
+                            max_cands: int, device):
+    """Workspace of hstu_cand_kv4_fwd for these sizes; with as many heads it serves
+    every call of no larger ones."""
+    n = int(load_library().hstu_cand_kv4_workspace_size(int(batch), int(num_heads),
+                                                        int(max_seq_len), int(total_cands),
+                                                        int(max_cands)))
+    if n == 0:
+        raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_cand_kv4_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets, max_cands: int, *,
+                      first_rows=None, total_tokens=None, timestamps=None, cand_timestamps=None,
+                      rab_pos=None, rab_time=None, norm_len=0, eps=1e-5, ln_weight=None,
+                      ln_bias=None, offsets_host=None, y=None, workspace=None, stream=None):
+    """hstu_cand_fwd against histories in a 4-bit cache (hstu_kv4_pack): user b's
+    history is the cache rows first_rows[b].. (int32 [B]), or, without
+    first_rows, the rows offsets[b]..offsets[b+1]-1.  total_tokens bounds
+    offsets[B] (default: the timestamps' length, else the cache's rows, or, with
+    first_rows, no bound).  Returns y [C, H*128]."""
+    lib = load_library()
+    R, HC = _check_cache(cache)
+    for name, t in (("q", q), ("k", k), ("v", v), ("u", u)):
+        _dev(t, name, torch.bfloat16)
+    for name, t in (("offsets", offsets), ("cand_offsets", cand_offsets),
+                    ("first_rows", first_rows)):
+        _dev(t, name, torch.int32)
+    for name, t in (("timestamps", timestamps), ("cand_timestamps", cand_timestamps)):
+        _dev(t, name, torch.int64)
+    for name, t in (("rab_pos", rab_pos), ("rab_time", rab_time), ("ln_weight", ln_weight),
+                    ("ln_bias", ln_bias)):
+        _dev(t, name, torch.float32)
+    C, H, _ = q.shape
+    B = offsets.numel() - 1
+    if H != HC:
+        raise ValueError("the cache has %d heads, q has %d" % (HC, H))
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _shape(t, name, C, H, 128)
+    _shape(u, "u", C, H * 128)
+    _shape(cand_offsets, "cand_offsets", B + 1)
+    _shape(first_rows, "first_rows", B)
+    _shape(cand_timestamps, "cand_timestamps", C)
+    _shape(ln_weight, "ln_weight", H * 128)
+    _shape(ln_bias, "ln_bias", H * 128)
+    for name, t in (("rab_pos", rab_pos), ("rab_time", rab_time)):
+        if t is not None and (t.dim() != 2 or t.shape[0] != H):
+            raise ValueError("%s must have %d rows" % (name, H))
+    if rab_pos is not None and rab_pos.shape[1] % 2 != 1:
+        raise ValueError("rab_pos must be [H, 2L - 1]")
+    limit = (timestamps.numel() if timestamps is not None else
+             R if first_rows is None else 2 ** 31 - 1)
+    if total_tokens is None:
+        total_tokens = limit
+    elif timestamps is not None and total_tokens > limit:
+        raise ValueError("total_tokens exceeds the timestamps' length")
+    with _on(q, *cache, offsets, k, v, u, cand_offsets, first_rows, timestamps, cand_timestamps,
+             rab_pos, rab_time, ln_weight, ln_bias, y, workspace):
+        p = make_problem(q, v, offsets, max_seq_len, timestamps, rab_pos, rab_time, norm_len, eps,
+                         None, ln_weight, ln_bias)
+        p.total_tokens = int(total_tokens)
+        if timestamps is not None and rab_time is not None and timestamps.numel() == 0:
+            p.timestamps = rab_time.data_ptr()   # nothing to read; an empty tensor has no address
+        if offsets_host is not None:
+            p.total_tokens = int(offsets_host[-1])
+            p.offsets_host = offsets_host.data_ptr()
+        if y is None:
+            y = torch.empty((C, H * 128), dtype=q.dtype, device=q.device)
+        _dev(y, "y", q.dtype)
+        _shape(y, "y", C, H * 128)
+        if workspace is None:
+            workspace = hstu_cand_kv4_workspace(B, H, max_seq_len, C, max_cands, q.device)
+        rc = lib.hstu_cand_kv4_fwd(ctypes.byref(p), *[_ptr(t) for t in cache], R,
+                                   _ptr(first_rows), _ptr(cand_offsets), C, int(max_cands),
+                                   _ptr(cand_timestamps), _ptr(q), _ptr(k), _ptr(v), _ptr(u),
+                                   _ptr(y), _ptr(workspace), workspace.numel(),
+                                   _stream_ptr(stream))
+    if rc != HSTU_OK:
+        raise HSTUError(rc, "hstu_cand_kv4_fwd")
     return y

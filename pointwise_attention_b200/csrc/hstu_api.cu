@@ -133,6 +133,21 @@ bool make_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
   return r == CUDA_SUCCESS;
 }
 
+// [rows, cols] bytes row-major as a 2-D tensor (col, row); box = 128 x box_rows,
+// 128-byte swizzle.  Rows past `rows` and columns past `cols` read as zeros.
+bool make_map_2d_u8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------- validation
 hstu_status_t check_problem(const hstu_problem_t* p) {
   if (!p) return HSTU_ERR_INVALID_ARG;
@@ -517,6 +532,46 @@ hstu_status_t hstu_uvqk_fwd(int32_t T, int32_t E, int32_t H, int32_t d_qk, int32
   return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
+hstu_status_t hstu_uvqk_fp8_fwd(int32_t T, int32_t E, int32_t H, int32_t d_qk, int32_t d_v,
+                                int32_t act, const uint8_t* x8, const float* x_scale,
+                                const uint8_t* w8, const float* w_scale, const float* bias,
+                                void* u, void* v, void* q, void* k, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  NvtxRange range("hstu_uvqk_fp8_fwd");
+  if (T < 0 || E < 1 || H < 1 || d_qk < 1 || d_v < 1 || (act != 0 && act != 1))
+    return HSTU_ERR_INVALID_ARG;
+  if (T > 0) {
+    const void* ptrs[] = {x8, x_scale, w8, w_scale, u, v, q, k};
+    for (const void* p : ptrs)
+      if (!p || !aligned16(p)) return HSTU_ERR_INVALID_ARG;
+    if (bias && !aligned16(bias)) return HSTU_ERR_INVALID_ARG;
+  }
+  const int64_t Nu = static_cast<int64_t>(H) * d_v, Nq = static_cast<int64_t>(H) * d_qk;
+  if (E % 16 != 0 || Nu % 256 != 0 || Nq % 256 != 0 || 2 * (Nu + Nq) > 65535 * 256 ||
+      (static_cast<int64_t>(T) + 127) / 128 > 65535)
+    return HSTU_ERR_UNSUPPORTED;
+  hstu_status_t st = check_status_ws(workspace, workspace_bytes);
+  if (st != HSTU_OK) return st;
+  if (T == 0) return HSTU_OK;
+  Proj8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.x_scale = x_scale;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.out0 = u; a.out1 = v; a.out2 = q; a.out3 = k;
+  a.status = static_cast<int*>(workspace);
+  a.T = T; a.E = E;
+  a.Nu = static_cast<int>(Nu); a.Nq = static_cast<int>(Nq);
+  a.act = act;
+  a.vec32 = al32(u) && al32(v) && al32(q) && al32(k);
+  const int N = static_cast<int>(2 * (Nu + Nq));
+  CUtensorMap tx, tw;
+  if (!make_map_2d_u8(&tx, x8, T, E, 128) || !make_map_2d_u8(&tw, w8, N, E, uvqk_fp8_cols(T, N)))
+    return HSTU_ERR_CUDA;
+  const cudaError_t err = launch_uvqk_fp8_sm100(a, tx, tw, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
 hstu_status_t hstu_out_fwd(int32_t T, int32_t E, int32_t D, const void* y, const void* w,
                            const void* x, const float* bias, const float* ln_weight,
                            const float* ln_bias, float eps, void* z, float* mean, float* rstd,
@@ -653,6 +708,92 @@ hstu_status_t hstu_cand_fwd(const hstu_problem_t* p, const void* k_hist, const v
     err = launch_cand_plans(a, static_cast<cudaStream_t>(stream));
   if (err == cudaSuccess) err = launch_cand_order(a, static_cast<cudaStream_t>(stream));
   if (err == cudaSuccess) err = launch_cand_sm100(a, tq, tk, tv, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+// ---------------------------------------------------------- candidates, 4-bit cache
+size_t hstu_cand_kv4_workspace_size(int32_t batch, int32_t num_heads, int32_t max_seq_len,
+                                    int32_t total_cands, int32_t max_cands) {
+  if (batch < 0 || num_heads < 1 || num_heads > 16 || max_seq_len < 0 || total_cands < 0 ||
+      max_cands < 0)
+    return 0;
+  return kStatusBytes + align_up(cand4_part_rows(num_heads, max_seq_len, total_cands) *
+                                 static_cast<size_t>(num_heads) * 512);
+}
+
+hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, const void* k_scales,
+                                const void* v_codes, const void* v_scales, int32_t cache_rows,
+                                const int32_t* first_rows, const int32_t* cand_offsets,
+                                int32_t total_cands, int32_t max_cands,
+                                const int64_t* cand_timestamps, const void* q, const void* k,
+                                const void* v, const void* u, void* y, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  NvtxRange range("hstu_cand_kv4_fwd");
+  hstu_status_t st = check_problem(p);
+  if (st != HSTU_OK) return st;
+  if (total_cands < 0 || max_cands < 0 || cache_rows < 0 || (total_cands > 0 && max_cands < 1))
+    return HSTU_ERR_INVALID_ARG;
+  if (!first_rows && cache_rows < p->total_tokens) return HSTU_ERR_INVALID_ARG;
+  if (p->batch > 0 && !cand_offsets) return HSTU_ERR_INVALID_ARG;
+  if (p->rab_pos && p->rab_pos_len <= p->max_seq_len) return HSTU_ERR_INVALID_ARG;
+  if (p->rab_time && total_cands > 0 && !cand_timestamps) return HSTU_ERR_INVALID_ARG;
+  if (total_cands > 0) {
+    const void* ptrs[] = {q, k, v, u, y};
+    for (const void* x : ptrs)
+      if (!x || !aligned16(x)) return HSTU_ERR_INVALID_ARG;
+  }
+  if (p->total_tokens > 0) {
+    const void* ptrs[] = {k_codes, k_scales, v_codes, v_scales};
+    for (const void* x : ptrs)
+      if (!x || !aligned16(x)) return HSTU_ERR_INVALID_ARG;
+  }
+  if (p->dtype != HSTU_BF16 || p->d_qk != 128 || p->d_v != 128 || p->num_heads > 16)
+    return HSTU_ERR_UNSUPPORTED;
+  const Cand4Cut cut = cand4_cut(p->batch, p->num_heads, p->max_seq_len, max_cands);
+  // one grid dimension holds every (user, candidates, keys, heads) CTA, and
+  // every (user, candidate)
+  if (static_cast<double>(p->batch) * cut.cgroups * cut.splits * cut.hgroups > 2147483647.0 ||
+      static_cast<double>(p->batch) * max_cands > 2147483647.0)
+    return HSTU_ERR_UNSUPPORTED;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
+      workspace_bytes < hstu_cand_kv4_workspace_size(p->batch, p->num_heads, p->max_seq_len,
+                                                     total_cands, max_cands))
+    return HSTU_ERR_WORKSPACE;
+  if (p->batch == 0 || total_cands == 0) return HSTU_OK;
+
+  Cand4Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.offsets = p->offsets;
+  a.cand_offsets = cand_offsets;
+  a.first_rows = first_rows;
+  a.timestamps = p->timestamps;
+  a.cand_ts = cand_timestamps;
+  a.rab_pos = p->rab_pos;
+  a.rab_time = p->rab_time;
+  a.k_codes = static_cast<const uint8_t*>(k_codes);
+  a.k_scales = static_cast<const uint16_t*>(k_scales);
+  a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.v_scales = static_cast<const uint16_t*>(v_scales);
+  a.q = q; a.k = k; a.v = v; a.u = u; a.y = y;
+  a.ln_weight = p->ln_weight;
+  a.ln_bias = p->ln_bias;
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+  a.status = static_cast<int*>(workspace);
+  a.B = p->batch;
+  a.T = p->total_tokens;
+  a.C = total_cands;
+  a.H = p->num_heads;
+  a.R = cache_rows;
+  a.max_seq_len = p->max_seq_len;
+  a.max_cands = max_cands;
+  a.L = p->rab_pos ? p->rab_pos_len : 0;
+  a.nb = p->rab_time ? p->num_time_buckets : 0;
+  a.norm_len = p->norm_len;
+  a.eps = p->ln_eps;
+  a.chunk = cut.chunk;
+  a.splits = cut.splits;
+  fill_bucket_table(&a.bt, p->rab_time ? p->num_time_buckets : 1);
+  const cudaError_t err = launch_cand4_few(a, cut, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 

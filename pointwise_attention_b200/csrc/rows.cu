@@ -1,0 +1,505 @@
+// rows.cu -- row operators ahead of an HSTU layer's projection: the
+// root-mean-square norm with the residual's addition (forward and backward)
+// and the quantisation of rows to 8 bits (e4m3 with one scale per row).
+//
+//   h_te = round(x_te + res_te)                    (the residual stream's type)
+//   r_t  = 1 / sqrt(mean_e h_te^2 + eps)
+//   v_te = h_te r_t w_e
+//   y    = round(v)   or   q8 = e4m3(v / s_t),  s_t = max(max_e |v_te|, 2^-100) / 448
+//
+//   g = w dy;  dx = dres + r (g - h r^2 mean_e(g h));  dw_e = sum_t dy_te h_te r_t
+//
+// Every operator is one pass over its rows: a row lives in the registers of
+// the TPR threads that own it (NV vectors of VEC elements each), so that each
+// input is read once and each output written once; what bounds them is HBM.
+// Sums, statistics and products are fp32.  h is rounded to the stream's type
+// before the norm because that is the value which the next layer and the
+// backward read; y and q8 take v unrounded.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "hstu.h"
+#include "internal.h"
+
+namespace hstu {
+namespace {
+
+constexpr int kMaxE = 16384;
+constexpr float kE4M3Max = 448.0f;
+constexpr float kAmaxFloor = 7.8886090522101181e-31f;   // 2^-100: keeps 1 / scale finite
+
+struct RowsArgs {
+  const void* x;
+  const void* res;       // or null
+  const float* weight;   // [E] or null (ones)
+  void* h;               // or null
+  void* y;               // or null
+  uint8_t* q8;           // or null (with scale)
+  float* scale;
+  float* rstd;           // or null
+  int T, E;
+  float eps;
+};
+
+struct RowsBwdArgs {
+  const void* dy;
+  const void* h;
+  const float* weight;   // [E] or null (ones)
+  const float* rstd;
+  const void* dres;      // or null
+  void* dx;
+  float* partial;        // [gridDim.x][E], or null: no weight gradient
+  int T, E;
+};
+
+template <typename T> struct Elem;
+template <> struct Elem<float> {
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <> struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+  T v[VEC];
+};
+
+// The vectors of one row that this thread owns: vector i sits at column
+// (i TPR + lane) VEC; columns at or past E read as zeros.
+template <typename T, int VEC, int TPR, int NV>
+__device__ __forceinline__ void load_row(const T* row, int lane, int E, Pack<T, VEC> (&p)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + lane) * VEC;
+    if (c < E) {
+      p[i] = *reinterpret_cast<const Pack<T, VEC>*>(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) p[i].v[e] = Elem<T>::put(0.f);
+    }
+  }
+}
+
+template <int VEC, int TPR, int NV>
+__device__ __forceinline__ void load_weight(const float* w, int lane, int E, float (&r)[NV * VEC]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + lane) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) r[i * VEC + e] = 1.f;
+    if (w && c < E) {
+      if (VEC >= 4) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(w + c + e));
+          r[i * VEC + e] = f.x;
+          r[i * VEC + e + 1] = f.y;
+          r[i * VEC + e + 2] = f.z;
+          r[i * VEC + e + 3] = f.w;
+        }
+      } else {
+        r[i * VEC] = __ldg(w + c);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum (or, for bit patterns of non-negative floats, maximum) over the TPR
+// threads of a row.  TPR > 32: the block is the row.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if (TPR > 32) {
+    __syncthreads();   // red may still be read by the row before
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) v += red[i];
+  }
+  return v;
+}
+
+template <int TPR>
+__device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (TPR > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) v = max(v, red[i]);
+  }
+  return v;
+}
+
+template <int TPR>
+constexpr int block_threads() { return TPR == 32 ? 256 : TPR; }
+
+// NORM: the norm; otherwise the rows as they are (quantisation alone).
+template <typename T, int VEC, int TPR, int NV, bool NORM>
+__global__ void __launch_bounds__(block_threads<TPR>()) hstu_rows_fwd(const RowsArgs a) {
+  constexpr int kRows = block_threads<TPR>() / TPR;   // rows of a block at a time
+  constexpr int N = NV * VEC;
+  __shared__ float red[TPR > 32 ? TPR / 32 : 1];
+  const int lane = TPR == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+  const int sub = TPR == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.res);
+  float w[N];
+  if (NORM) load_weight<VEC, TPR, NV>(a.weight, lane, a.E, w);
+  // the loop is uniform over the threads of a row, and over the block where
+  // the block is the row
+  for (int t = static_cast<int>(blockIdx.x) * kRows + sub; t < a.T;
+       t += static_cast<int>(gridDim.x) * kRows) {
+    const size_t at = static_cast<size_t>(t) * a.E;
+    Pack<T, VEC> p[NV];
+    load_row<T, VEC, TPR, NV>(x + at, lane, a.E, p);
+    if (NORM && res) {
+      Pack<T, VEC> q[NV];
+      load_row<T, VEC, TPR, NV>(res + at, lane, a.E, q);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          p[i].v[e] = Elem<T>::put(Elem<T>::get(p[i].v[e]) + Elem<T>::get(q[i].v[e]));
+      if (a.h) {
+        T* h = static_cast<T*>(a.h) + at;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * TPR + lane) * VEC;
+          if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(h + c) = p[i];
+        }
+      }
+    }
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = Elem<T>::get(p[i / VEC].v[i % VEC]);
+    if (NORM) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) ss = fmaf(v[i], v[i], ss);
+      ss = row_sum<TPR>(ss, red);
+      const float r = 1.0f / sqrtf(ss / static_cast<float>(a.E) + a.eps);
+      if (a.rstd && lane == 0) a.rstd[t] = r;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] * r * w[i];
+      if (a.y) {
+        T* y = static_cast<T*>(a.y) + at;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * TPR + lane) * VEC;
+          Pack<T, VEC> o;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) o.v[e] = Elem<T>::put(v[i * VEC + e]);
+          if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(y + c) = o;
+        }
+      }
+    }
+    if (!NORM || a.q8) {
+      // The maximum goes over bit patterns: those of |v| are ordered like the
+      // values, with NaN above infinity, so that a NaN reaches the scale.
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      m = row_umax<TPR>(m, reinterpret_cast<uint32_t*>(red));
+      const float top = __uint_as_float(m);
+      const float s = (top < kAmaxFloor ? kAmaxFloor : top) / kE4M3Max;
+      const float inv = 1.0f / s;
+      if (lane == 0) a.scale[t] = s;
+      uint8_t* q8 = a.q8 + at;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * VEC;
+        Pack<uint8_t, VEC> o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          o.v[e] = __nv_cvt_float_to_fp8(v[i * VEC + e] * inv, __NV_SATFINITE, __NV_E4M3);
+        if (c < a.E) *reinterpret_cast<Pack<uint8_t, VEC>*>(q8 + c) = o;
+      }
+    }
+  }
+}
+
+template <typename T, int VEC, int TPR, int NV>
+__global__ void __launch_bounds__(block_threads<TPR>()) hstu_rows_bwd(const RowsBwdArgs a) {
+  constexpr int kRows = block_threads<TPR>() / TPR;
+  constexpr int N = NV * VEC;
+  __shared__ float red[TPR > 32 ? TPR / 32 : 1];
+  __shared__ float sdw[TPR == 32 ? kRows : 1][TPR == 32 ? 32 * N : 1];
+  const int lane = TPR == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+  const int sub = TPR == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  float w[N], dw[N];
+  load_weight<VEC, TPR, NV>(a.weight, lane, a.E, w);
+#pragma unroll
+  for (int i = 0; i < N; ++i) dw[i] = 0.f;
+  for (int t = static_cast<int>(blockIdx.x) * kRows + sub; t < a.T;
+       t += static_cast<int>(gridDim.x) * kRows) {
+    const size_t at = static_cast<size_t>(t) * a.E;
+    Pack<T, VEC> pd[NV], ph[NV], pr[NV];
+    load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.dy) + at, lane, a.E, pd);
+    load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.h) + at, lane, a.E, ph);
+    if (a.dres) load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.dres) + at, lane, a.E, pr);
+    const float r = __ldg(a.rstd + t);
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float d = Elem<T>::get(pd[i / VEC].v[i % VEC]), h = Elem<T>::get(ph[i / VEC].v[i % VEC]);
+      dot = fmaf(d * w[i], h, dot);
+      dw[i] = fmaf(d * h, r, dw[i]);
+    }
+    dot = row_sum<TPR>(dot, red);
+    const float k = r * r * (dot / static_cast<float>(a.E));
+    T* dx = static_cast<T*>(a.dx) + at;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * VEC;
+      Pack<T, VEC> o;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = Elem<T>::get(pd[i].v[e]), h = Elem<T>::get(ph[i].v[e]);
+        float g = r * fmaf(-h, k, d * w[i * VEC + e]);
+        if (a.dres) g += Elem<T>::get(pr[i].v[e]);
+        o.v[e] = Elem<T>::put(g);
+      }
+      if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(dx + c) = o;
+    }
+  }
+  if (!a.partial) return;
+  float* part = a.partial + static_cast<size_t>(blockIdx.x) * a.E;
+  if (TPR == 32) {
+    // the warps' sums of the block, added in warp order
+#pragma unroll
+    for (int i = 0; i < N; ++i) sdw[sub][(i / VEC * 32 + lane) * VEC + i % VEC] = dw[i];
+    __syncthreads();
+    for (int c = static_cast<int>(threadIdx.x); c < a.E; c += block_threads<TPR>()) {
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < kRows; ++g) s += sdw[g][c];
+      part[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i / VEC * TPR + lane) * VEC + i % VEC;
+      if (c < a.E) part[c] = dw[i];
+    }
+  }
+}
+
+// dw[c] = the blocks' partial sums added in a fixed order: 32 columns by 32
+// block strides per CTA.
+__global__ void __launch_bounds__(1024) hstu_rows_dw(const float* partial, int blocks, int E,
+                                                     float* dw) {
+  __shared__ float red[32][33];
+  const int cx = static_cast<int>(threadIdx.x & 31), gy = static_cast<int>(threadIdx.x >> 5);
+  const int c = static_cast<int>(blockIdx.x) * 32 + cx;
+  float s = 0.f;
+  if (c < E)
+    for (int g = gy; g < blocks; g += 32) s += partial[static_cast<size_t>(g) * E + c];
+  red[gy][cx] = s;
+  __syncthreads();
+  s = warp_sum(red[cx][gy]);   // column gy of the tile
+  if (cx == 0 && static_cast<int>(blockIdx.x) * 32 + gy < E) dw[blockIdx.x * 32 + gy] = s;
+}
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// One row shape of the kernels: elements per vector, threads per row, vectors
+// per thread.  The smallest that holds E columns is taken: a warp per row up
+// to 1024 columns (8 rows a block, no barrier), 128 threads up to 4096, 512
+// up to 16384.  Rows whose columns or addresses do not divide into 16-byte
+// vectors take one element at a time.
+template <int VEC_, int TPR_, int NV_>
+struct Shape {
+  static constexpr int VEC = VEC_, TPR = TPR_, NV = NV_;
+};
+
+template <typename T, typename F>
+cudaError_t pick_shape(bool vec, int E, F&& f) {
+  if constexpr (sizeof(T) == 2) {
+    if (vec) {
+      if (E <= 256) return f(Shape<8, 32, 1>{});
+      if (E <= 512) return f(Shape<8, 32, 2>{});
+      if (E <= 1024) return f(Shape<8, 32, 4>{});
+      if (E <= 2048) return f(Shape<8, 128, 2>{});
+      if (E <= 4096) return f(Shape<8, 128, 4>{});
+      if (E <= 8192) return f(Shape<8, 512, 2>{});
+      return f(Shape<8, 512, 4>{});
+    }
+  } else {
+    if (vec) {
+      if (E <= 128) return f(Shape<4, 32, 1>{});
+      if (E <= 256) return f(Shape<4, 32, 2>{});
+      if (E <= 512) return f(Shape<4, 32, 4>{});
+      if (E <= 1024) return f(Shape<4, 32, 8>{});
+      if (E <= 2048) return f(Shape<4, 128, 4>{});
+      if (E <= 4096) return f(Shape<4, 128, 8>{});
+      if (E <= 8192) return f(Shape<4, 512, 4>{});
+      return f(Shape<4, 512, 8>{});
+    }
+  }
+  if (E <= 256) return f(Shape<1, 32, 8>{});
+  if (E <= 1024) return f(Shape<1, 32, 32>{});
+  if (E <= 2048) return f(Shape<1, 128, 16>{});
+  if (E <= 4096) return f(Shape<1, 128, 32>{});
+  return f(Shape<1, 512, 32>{});
+}
+
+template <typename T, bool NORM>
+cudaError_t launch_rows_fwd(const RowsArgs& a, cudaStream_t stream) {
+  constexpr size_t V = 16;
+  const bool vec = a.E % (V / sizeof(T)) == 0 && aligned(a.x, V) && aligned(a.res, V) &&
+                   aligned(a.h, V) && aligned(a.y, V) && aligned(a.q8, V / sizeof(T)) &&
+                   aligned(a.weight, V);
+  return pick_shape<T>(vec, a.E, [&](auto s) {
+    using S = decltype(s);
+    constexpr int kRows = block_threads<S::TPR>() / S::TPR;
+    const int blocks = static_cast<int>((static_cast<int64_t>(a.T) + kRows - 1) / kRows);
+    hstu_rows_fwd<T, S::VEC, S::TPR, S::NV, NORM>
+        <<<blocks, block_threads<S::TPR>(), 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+// Blocks of the backward: enough rows each that the partial sums stay small
+// beside the rows.  A function of the sizes alone (not of the device), so that
+// the order of the sums is too.
+int bwd_blocks(int T, int E) {
+  const int rows = E <= 1024 ? 8 : 1;
+  const int most = E <= 1024 ? 3 * 148 : E <= 4096 ? 6 * 148 : 2 * 148;
+  const int64_t need = (static_cast<int64_t>(T) + rows - 1) / rows;
+  return static_cast<int>(need < most ? need : most);
+}
+
+template <typename T>
+cudaError_t launch_rows_bwd(const RowsBwdArgs& a, float* dw, cudaStream_t stream) {
+  constexpr size_t V = 16;
+  const bool vec = a.E % (V / sizeof(T)) == 0 && aligned(a.dy, V) && aligned(a.h, V) &&
+                   aligned(a.dres, V) && aligned(a.dx, V) && aligned(a.weight, V);
+  const int blocks = bwd_blocks(a.T, a.E);
+  const cudaError_t err = pick_shape<T>(vec, a.E, [&](auto s) {
+    using S = decltype(s);
+    hstu_rows_bwd<T, S::VEC, S::TPR, S::NV><<<blocks, block_threads<S::TPR>(), 0, stream>>>(a);
+    return cudaGetLastError();
+  });
+  if (err != cudaSuccess || !dw) return err;
+  hstu_rows_dw<<<(a.E + 31) / 32, 1024, 0, stream>>>(a.partial, blocks, a.E, dw);
+  return cudaGetLastError();
+}
+
+size_t elem_bytes(hstu_dtype_t d) { return d == HSTU_BF16 ? 2 : 4; }
+
+hstu_status_t check_rows(hstu_dtype_t dtype, int32_t T, int32_t E) {
+  if ((dtype != HSTU_F32 && dtype != HSTU_BF16) || T < 0 || E < 1) return HSTU_ERR_INVALID_ARG;
+  return HSTU_OK;
+}
+
+struct RowsRange {
+  explicit RowsRange(const char* name) { nvtxRangePushA(name); }
+  ~RowsRange() { nvtxRangePop(); }
+};
+
+}  // namespace
+}  // namespace hstu
+
+using namespace hstu;
+
+extern "C" {
+
+HSTU_API hstu_status_t hstu_rmsnorm_fwd(hstu_dtype_t dtype, int32_t T, int32_t E, const void* x,
+                                        const void* residual, const float* weight, float eps,
+                                        void* h, void* y, uint8_t* q8, float* q8_scale,
+                                        float* rstd, void* stream) {
+  RowsRange range("hstu_rmsnorm_fwd");
+  const hstu_status_t st = check_rows(dtype, T, E);
+  if (st != HSTU_OK) return st;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return HSTU_ERR_INVALID_ARG;
+  if ((q8 == nullptr) != (q8_scale == nullptr)) return HSTU_ERR_INVALID_ARG;
+  if (h && !residual) return HSTU_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!x || (!y && !q8)) return HSTU_ERR_INVALID_ARG;
+    const size_t b = elem_bytes(dtype);
+    if (!aligned(x, b) || !aligned(residual, b) || !aligned(h, b) || !aligned(y, b))
+      return HSTU_ERR_INVALID_ARG;
+  }
+  if (!aligned(weight, 4) || !aligned(q8_scale, 4) || !aligned(rstd, 4))
+    return HSTU_ERR_INVALID_ARG;
+  if (E > kMaxE) return HSTU_ERR_UNSUPPORTED;
+  if (T == 0) return HSTU_OK;
+  const RowsArgs a{x, residual, weight, h, y, q8, q8_scale, rstd, T, E, eps};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t err = dtype == HSTU_BF16 ? launch_rows_fwd<__nv_bfloat16, true>(a, s)
+                                             : launch_rows_fwd<float, true>(a, s);
+  return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+HSTU_API hstu_status_t hstu_quant_rows(hstu_dtype_t dtype, int32_t T, int32_t E, const void* x,
+                                       uint8_t* q8, float* q8_scale, void* stream) {
+  RowsRange range("hstu_quant_rows");
+  const hstu_status_t st = check_rows(dtype, T, E);
+  if (st != HSTU_OK) return st;
+  if (T > 0 && (!x || !q8 || !q8_scale || !aligned(x, elem_bytes(dtype)) || !aligned(q8_scale, 4)))
+    return HSTU_ERR_INVALID_ARG;
+  if (E > kMaxE) return HSTU_ERR_UNSUPPORTED;
+  if (T == 0) return HSTU_OK;
+  const RowsArgs a{x, nullptr, nullptr, nullptr, nullptr, q8, q8_scale, nullptr, T, E, 1.0f};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t err = dtype == HSTU_BF16 ? launch_rows_fwd<__nv_bfloat16, false>(a, s)
+                                             : launch_rows_fwd<float, false>(a, s);
+  return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+HSTU_API size_t hstu_rmsnorm_bwd_workspace_size(int32_t T, int32_t E) {
+  if (T < 0 || E < 1 || E > kMaxE) return 0;
+  const size_t n = static_cast<size_t>(bwd_blocks(T, E)) * E * sizeof(float);
+  return n < 256 ? 256 : (n + 255) / 256 * 256;
+}
+
+HSTU_API hstu_status_t hstu_rmsnorm_bwd(hstu_dtype_t dtype, int32_t T, int32_t E, const void* dy,
+                                        const void* h, const float* rstd, const float* weight,
+                                        const void* d_residual, void* dx, float* d_weight,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  RowsRange range("hstu_rmsnorm_bwd");
+  const hstu_status_t st = check_rows(dtype, T, E);
+  if (st != HSTU_OK) return st;
+  if (T > 0) {
+    const size_t b = elem_bytes(dtype);
+    if (!dy || !h || !rstd || !dx || !aligned(dy, b) || !aligned(h, b) || !aligned(dx, b) ||
+        !aligned(d_residual, b))
+      return HSTU_ERR_INVALID_ARG;
+  }
+  if (!aligned(rstd, 4) || !aligned(weight, 4) || !aligned(d_weight, 4)) return HSTU_ERR_INVALID_ARG;
+  if (E > kMaxE) return HSTU_ERR_UNSUPPORTED;
+  if (d_weight && (!workspace || !aligned(workspace, 256) ||
+                   workspace_bytes < hstu_rmsnorm_bwd_workspace_size(T, E)))
+    return HSTU_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    // no rows: the weight's gradient is an empty sum
+    if (d_weight && cudaMemsetAsync(d_weight, 0, sizeof(float) * E, s) != cudaSuccess)
+      return HSTU_ERR_CUDA;
+    return HSTU_OK;
+  }
+  const RowsBwdArgs a{dy, h, weight, rstd, d_residual, dx,
+                      d_weight ? static_cast<float*>(workspace) : nullptr, T, E};
+  const cudaError_t err = dtype == HSTU_BF16 ? launch_rows_bwd<__nv_bfloat16>(a, d_weight, s)
+                                             : launch_rows_bwd<float>(a, d_weight, s);
+  return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+}  // extern "C"

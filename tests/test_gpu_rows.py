@@ -1,0 +1,290 @@
+"""GPU tests of the row operators (norm, its backward, 8-bit rows, the 8-bit
+UVQK projection) against their formulas in 64 bits.
+
+Tolerances count the roundings: half a step of the output's type relative to
+the value (bf16 2^-8, fp32 2^-24, e4m3 2^-4 and half of its smallest step,
+2^-10, near zero), and fp32 sums of n terms to n 2^-24 of the sum of their
+magnitudes.
+"""
+import pytest
+import torch
+
+import pointwise_attention_b200 as pa
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+HALF = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+EPS = 1e-6
+U = 2.0 ** -24
+
+
+def rows(seed, T, E, dtype, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (std * torch.randn(T, E, generator=g)).to(dtype).to(DEV)
+
+
+def within(got, ref, tol, what):
+    got, ref = got.double(), ref.double()
+    assert got.shape == ref.shape, what
+    assert torch.isfinite(got).all(), what
+    bad = (got - ref).abs() - tol
+    assert bool((bad <= 0).all()), "%s: off by %.3e over %.3e" % (
+        what, float((got - ref).abs().max()), float(bad.max()))
+
+
+def norm64(x, res, w, dtype):
+    h = x if res is None else (x.double() + res.double()).to(dtype)
+    hd = h.double()
+    r = 1.0 / torch.sqrt((hd * hd).mean(1) + EPS)
+    v = hd * r[:, None]
+    return h, r, v if w is None else v * w.double()
+
+
+def check_q8(q8, scale, v, E, what):
+    top = v.abs().amax(1).clamp_min(2.0 ** -100)
+    rel = (E + 16) * U
+    within(scale, top / 448.0, rel * top / 448.0, what + " scale")
+    # half a step of e4m3 relative to the value, at least half its smallest
+    # step; the value before the rounding is off by fp32's share
+    s = scale.double()[:, None]
+    within(q8.double() * s, v, v.abs() * (2.0 ** -4 + 3 * rel) + s * 2.0 ** -10 * (1 + rel), what)
+
+
+SHAPES = [(1, 1), (1, 16), (3, 7), (5, 256), (17, 512), (9, 513), (8, 1000), (33, 1024), (6, 1032),
+          (4, 2048), (3, 2055), (2, 4096), (3, 5000), (2, 8192), (2, 8200), (2, 16384), (1, 16383),
+          (1025, 64)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E", SHAPES)
+def test_norm_forward(T, E, dtype):
+    x, res = rows(T + E, T, E, dtype), rows(T + E + 1, T, E, dtype)
+    w = (1.0 + 0.3 * rows(3, 1, E, F32)[0])
+    rel = (E + 16) * U
+    for r_, w_ in ((res, w), (None, w), (res, None)):
+        h, rstd, v = norm64(x, r_, w_, dtype)
+        out = pa.hstu_rmsnorm_fwd(x, residual=r_, weight=w_, eps=EPS, save_rstd=True)
+        if r_ is None:
+            assert out["h"] is None
+        else:
+            assert torch.equal(out["h"], h)
+        assert out["q8"] is None
+        within(out["rstd"], rstd, rel * rstd, "rstd")
+        within(out["y"], v, v.abs() * (HALF[dtype] + 2 * rel), "y")
+        q = pa.hstu_rmsnorm_fwd(x, residual=r_, weight=w_, eps=EPS, quant=True)
+        assert q["y"] is None and q["rstd"] is None
+        check_q8(q["q8"], q["scale"], v, E, "q8")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E", SHAPES)
+def test_norm_backward(T, E, dtype):
+    h, dy, dres = (rows(s + E, T, E, dtype) for s in (1, 2, 3))
+    w = 1.0 + 0.3 * rows(3, 1, E, F32)[0]
+    rstd = (1.0 / torch.sqrt((h.double() ** 2).mean(1) + EPS)).float()
+    hd, dyd, r = h.double(), dy.double(), rstd.double()[:, None]
+    for w_, d_ in ((w, dres), (w, None), (None, dres)):
+        g = dyd if w_ is None else dyd * w_.double()
+        m = (g * hd).mean(1, keepdim=True)
+        dx = r * (g - hd * r * r * m)
+        dw = (dyd * hd * r).sum(0)
+        rel = (E + 16) * U
+        mabs = (g * hd).abs().mean(1, keepdim=True)
+        tol = r * (g.abs() * 4 * U + hd.abs() * r * r * mabs * rel)
+        if d_ is not None:
+            dx = dx + d_.double()
+            tol = tol + d_.double().abs() * 2 * U
+        got, gw = pa.hstu_rmsnorm_bwd(dy, h, rstd, weight=w_, d_residual=d_)
+        within(got, dx, tol + dx.abs() * (HALF[dtype] + 2 * U), "dx")
+        within(gw, dw, (dyd * hd * r).abs().sum(0) * (T + 8) * U, "dw")
+        got2, none = pa.hstu_rmsnorm_bwd(dy, h, rstd, weight=w_, d_residual=d_,
+                                         need_weight_grad=False)
+        assert none is None and torch.equal(got, got2)
+
+
+def test_norm_backward_against_differences():
+    """The gradients are those of the forward: central differences in 64 bits
+    of L = sum(y c) + sum(h e)."""
+    T, E = 3, 40
+    x, res, c, e = (rows(s, T, E, F32) for s in (1, 2, 3, 4))
+    w = 1.0 + 0.3 * rows(5, 1, E, F32)[0]
+    out = pa.hstu_rmsnorm_fwd(x, residual=res, weight=w, eps=EPS, save_rstd=True)
+    dx, dw = pa.hstu_rmsnorm_bwd(c, out["h"], out["rstd"], weight=w, d_residual=e)
+
+    def loss(xd, wd):
+        h = xd + res.double()
+        v = h / torch.sqrt((h * h).mean(1, keepdim=True) + EPS) * wd
+        return float((v * c.double()).sum() + (h * e.double()).sum())
+
+    step = 1e-4   # differences are off by step^2 times third derivatives of order ten
+    for t, i in ((0, 0), (1, 17), (2, 39)):
+        d = torch.zeros(T, E, dtype=torch.float64, device=DEV)
+        d[t, i] = step
+        num = (loss(x.double() + d, w.double()) - loss(x.double() - d, w.double())) / (2 * step)
+        assert abs(num - float(dx[t, i])) <= 1e-6 + 1e-5 * abs(num)
+    for i in (0, 21, 39):
+        d = torch.zeros(E, dtype=torch.float64, device=DEV)
+        d[i] = step
+        num = (loss(x.double(), w.double() + d) - loss(x.double(), w.double() - d)) / (2 * step)
+        assert abs(num - float(dw[i])) <= 1e-6 + 1e-5 * abs(num)
+
+
+def test_norm_backward_many_rows_repeats_bitwise():
+    """More rows than blocks: each block walks several; the sums' order is fixed."""
+    T, E = 5003, 96
+    h, dy = rows(1, T, E, BF16), rows(2, T, E, BF16)
+    rstd = (1.0 / torch.sqrt((h.double() ** 2).mean(1) + EPS)).float()
+    dx, dw = pa.hstu_rmsnorm_bwd(dy, h, rstd)
+    terms = dy.double() * h.double() * rstd.double()[:, None]
+    within(dw, terms.sum(0), terms.abs().sum(0) * (T + 8) * U, "dw")
+    dx2, dw2 = pa.hstu_rmsnorm_bwd(dy, h, rstd)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E", SHAPES)
+def test_quant_rows(T, E, dtype):
+    x = rows(T * E, T, E, dtype)
+    q8, s = pa.hstu_quant_rows(x)
+    check_q8(q8, s, x.double(), E, "q8")
+
+
+def test_unaligned_rows_and_no_rows():
+    base = rows(1, 1, 6 * 64 + 1, BF16)[0]
+    x = base[1:].view(6, 64)                 # 2-byte aligned
+    out = pa.hstu_rmsnorm_fwd(x, eps=EPS)
+    ref = pa.hstu_rmsnorm_fwd(x.clone(), eps=EPS)
+    _, _, v = norm64(x, None, None, BF16)
+    for o in (out, ref):
+        within(o["y"], v, v.abs() * (HALF[BF16] + 200 * U), "y")
+    empty = torch.empty(0, 64, dtype=BF16, device=DEV)
+    assert pa.hstu_rmsnorm_fwd(empty)["y"].shape == (0, 64)
+    dx, dw = pa.hstu_rmsnorm_bwd(empty, empty, torch.empty(0, device=DEV))
+    assert dx.shape == (0, 64) and torch.equal(dw, torch.zeros(64, device=DEV))
+    assert pa.hstu_quant_rows(empty)[0].shape == (0, 64)
+
+
+def test_zero_rows_nan_rows_and_neighbours():
+    x = rows(1, 8, 128, BF16)
+    x[2] = 0.0
+    x[4, 100] = float("nan")
+    x[6, 3] = float("inf")
+    y = pa.hstu_rmsnorm_fwd(x, eps=EPS)["y"]
+    q = pa.hstu_rmsnorm_fwd(x, eps=EPS, quant=True)
+    assert torch.equal(y[2], torch.zeros_like(y[2])) and torch.isnan(y[4]).all()
+    assert torch.equal(q["q8"][2].float(), torch.zeros(128, device=DEV))
+    # the scale is the fp32 number nearest to 2^-100 / 448 (which is not one)
+    assert q["scale"][2].cpu() == torch.tensor(2.0 ** -100 / 448, dtype=F32)
+    assert torch.isnan(q["scale"][4])
+    for t in (0, 1, 3, 5, 7):
+        _, _, v = norm64(x[t:t + 1], None, None, BF16)
+        within(y[t:t + 1], v, v.abs() * (HALF[BF16] + 300 * U), "y")
+
+
+def test_outputs_over_inputs():
+    """The residual stream updated in place; dx over d_residual."""
+    x, res = rows(1, 77, 512, BF16), rows(2, 77, 512, BF16)
+    want = pa.hstu_rmsnorm_fwd(x, residual=res, eps=EPS, save_rstd=True)
+    res2 = res.clone()
+    got = pa.hstu_rmsnorm_fwd(x, residual=res2, eps=EPS, out=dict(h=res2))
+    assert torch.equal(got["h"], want["h"]) and got["h"].data_ptr() == res2.data_ptr()
+    assert torch.equal(got["y"], want["y"])
+    dy, dres = rows(3, 77, 512, BF16), rows(4, 77, 512, BF16)
+    dx, dw = pa.hstu_rmsnorm_bwd(dy, want["h"], want["rstd"], d_residual=dres)
+    d2 = dres.clone()
+    dx2, dw2 = pa.hstu_rmsnorm_bwd(dy, want["h"], want["rstd"], d_residual=d2, dx=d2)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+# ------------------------------------------------------------ 8-bit projection
+def silu64(x):
+    return x / (1.0 + torch.exp(-x))
+
+
+def project(seed, T, E, H, dqk, dv, act, bias, what):
+    N = 2 * H * (dqk + dv)
+    x8, xs = pa.hstu_quant_rows(rows(seed, T, E, F32))
+    w8, ws = pa.hstu_quant_rows(rows(seed + 1, N, E, F32, std=E ** -0.5))
+    b = 0.2 * rows(seed + 2, 1, N, F32)[0] if bias else None
+    status = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    out = pa.hstu_uvqk_fp8_fwd(x8, xs, w8, ws, H, dqk, dv, bias=b, act=act, workspace=status)
+    assert pa.hstu_attn_check(status) == 0
+    xd, wd = x8.double() * xs.double()[:, None], w8.double() * ws.double()[:, None]
+    p = xd @ wd.t()
+    mag = xd.abs() @ wd.abs().t()
+    if b is not None:
+        p = p + b.double()
+    # fp32 sums of E products, four roundings after them; SiLU's slope is at
+    # most 1.1 and its exponential and quotient are good to 2^-20
+    tol = mag * (E + 4) * U + p.abs() * 4 * U
+    if act:
+        p, tol = silu64(p), 1.1 * tol + silu64(p).abs() * 2.0 ** -20
+    tol = tol + p.abs() * HALF[BF16] + 1e-30
+    at = 0
+    for n, w_ in (("u", dv), ("v", dv), ("q", dqk), ("k", dqk)):
+        got = out[n].reshape(T, -1)
+        within(got, p[:, at:at + H * w_], tol[:, at:at + H * w_], what + " " + n)
+        at += H * w_
+    return out
+
+
+@pytest.mark.parametrize("T", [1, 17, 128, 129, 300])
+@pytest.mark.parametrize("E,H,dqk,dv,act,bias", [
+    (16, 2, 128, 128, 1, True), (64, 2, 128, 128, 0, False), (80, 4, 64, 128, 1, True),
+    (512, 4, 128, 128, 1, True), (528, 8, 128, 128, 0, True), (1040, 2, 128, 128, 1, False),
+    (256, 1, 256, 512, 1, True)])
+def test_uvqk_fp8(T, E, H, dqk, dv, act, bias):
+    project(T + E, T, E, H, dqk, dv, act, bias, "uvqk")
+
+
+@pytest.mark.parametrize("T", [1111, 5000, 40001])
+def test_uvqk_fp8_many_rows(T):
+    project(T, T, 192, 4, 128, 128, 1, True, "uvqk")
+
+
+def test_uvqk_fp8_outputs_stay_inside(monkeypatch):
+    """Rows behind the last token and unaligned-by-32 outputs: nothing else is
+    written."""
+    T, E, H = 70, 128, 2
+    x8, xs = pa.hstu_quant_rows(rows(1, T, E, F32))
+    w8, ws = pa.hstu_quant_rows(rows(2, 1024, E, F32))
+    ref = pa.hstu_uvqk_fp8_fwd(x8, xs, w8, ws, H, 128, 128, act=1)
+    big = {n: torch.full((T * 256 + 256 + 8,), 7.0, dtype=BF16, device=DEV) for n in "uvqk"}
+    out = {n: big[n][8:8 + T * 256].view((T, 256) if n == "u" else (T, 2, 128)) for n in "uvqk"}
+    pa.hstu_uvqk_fp8_fwd(x8, xs, w8, ws, H, 128, 128, act=1, out=out)
+    for n in "uvqk":
+        assert torch.equal(out[n], ref[n])
+        assert bool((big[n][:8] == 7).all()) and bool((big[n][8 + T * 256:] == 7).all())
+
+
+def test_capture_and_other_stream():
+    """Norm to 8 bits and projection captured in one graph, replayed on new
+    inputs on a side stream."""
+    T, E, H = 200, 256, 2
+    x = rows(1, T, E, BF16)
+    w8, ws = pa.hstu_quant_rows(rows(2, 1024, E, F32, std=0.1))
+    status = torch.zeros(256, dtype=torch.uint8, device=DEV)
+
+    def step():
+        n = pa.hstu_rmsnorm_fwd(x, eps=EPS, quant=True)
+        return pa.hstu_uvqk_fp8_fwd(n["q8"], n["scale"], w8, ws, H, 128, 128, act=1,
+                                    workspace=status)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for seed in (5, 6):
+        x.copy_(rows(seed, T, E, BF16))
+        g.replay()
+        torch.cuda.synchronize()
+        want = step()
+        for n in "uvqk":
+            assert torch.equal(out[n], want[n])
+    assert pa.hstu_attn_check(status) == 0
