@@ -379,7 +379,8 @@ HSTU_API int32_t hstu_pos_bucket_thresholds(int32_t *out, int32_t num_buckets, i
  * 0..T-1 when rows is NULL; other rows stay as they are.  hstu_kv4_unpack
  * reads rows back (a token of row -1 keeps its k, v).  Rows outside
  * [-1, cache_rows) are skipped and reported by hstu_attn_check.  All pointers
- * 16-byte aligned (rows: 4).  workspace: 256 bytes with the status word.
+ * 16-byte aligned (rows: 4).  workspace: 256 bytes with the status word; it may
+ * be NULL when rows is.
  */
 HSTU_API hstu_status_t hstu_kv4_pack(int32_t T, int32_t H, const void *k, const void *v,
                                      const int32_t *rows, int32_t cache_rows, void *k_codes,

@@ -8,6 +8,7 @@ not on a CUDA device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -404,25 +405,59 @@ def hstu_cand_fwd(k_hist, v_hist, offsets, max_seq_len, q, k, v, u, cand_offsets
     return y
 
 
-def _rows_dtype(t):
-    if t.dtype == torch.bfloat16:
-        return HSTU_BF16
-    if t.dtype == torch.float32:
-        return HSTU_F32
-    raise ValueError("rows must be bf16 or fp32")
+_BF16, _F32, _F8, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.float8_e4m3fn,
+                                     torch.int32, torch.int64, torch.uint8)
+_ROWS = {_BF16: HSTU_BF16, _F32: HSTU_F32}
+_STAY = contextlib.nullcontext()
 
 
-def _shape(t, name, *shape):
-    if t is not None and tuple(t.shape) != shape:
+def _rows_dtype(t, name):
+    """The library's name of the rows' type; t must be [T, E]."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ROWS:
+        raise ValueError("%s must be a bf16 or fp32 tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be [T, E]" % name)
+    return _ROWS[t.dtype]
+
+
+def _arg(t, name, dtype, *shape):
+    """Placement, layout, type and shape of one argument (None passes); its address."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the library runs on the GPU only)" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
+    if shape and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    return t.data_ptr()
 
 
 def _on(ref, *tensors):
     """A context in which ref's device is current; every tensor must be there."""
+    at = ref.get_device()
     for t in tensors:
-        if t is not None and t.device != ref.device:
+        if t is not None and t.get_device() != at:
             raise ValueError("all tensors must be on one device (%s and %s)" % (ref.device, t.device))
-    return torch.cuda.device(ref.device)
+    return _STAY if torch._C._cuda_getDevice() == at else torch.cuda.device(at)
+
+
+def _stream_of(ref, stream):
+    """The given stream, else the current one of ref's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(ref.get_device())
+
+
+def _room(workspace, ref):
+    """A workspace's address and bytes (a status word's worth when None)."""
+    if workspace is None:
+        workspace = _status_workspace(ref.device)
+    elif not workspace.is_cuda or workspace.dtype != _U8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def hstu_rmsnorm_fwd(x, *, residual=None, weight=None, eps: float = 1e-6, quant: bool = False,
@@ -433,40 +468,33 @@ def hstu_rmsnorm_fwd(x, *, residual=None, weight=None, eps: float = 1e-6, quant:
     quant q8 (e4m3) and scale (fp32 [T]); rstd (fp32 [T], None unless save_rstd).
     ``out`` may hold any of these tensors to write to."""
     lib = load_library()
-    _dev(x, "x")
-    dt = _rows_dtype(x)
-    _dev(residual, "residual", x.dtype)
-    _dev(weight, "weight", torch.float32)
-    if x.dim() != 2:
-        raise ValueError("x must be [T, E]")
+    dt = _rows_dtype(x, "x")
     T, E = x.shape
-    _shape(residual, "residual", T, E)
-    _shape(weight, "weight", E)
-    res = dict(h=None, y=None, q8=None, scale=None, rstd=None)
-    res.update(out or {})
-    with _on(x, residual, weight, *res.values()):
-        if residual is not None and res["h"] is None:
-            res["h"] = torch.empty_like(x)
+    xp = _arg(x, "x", x.dtype)
+    rp = _arg(residual, "residual", x.dtype, T, E)
+    wp = _arg(weight, "weight", _F32, E)
+    h = y = q8 = scale = rstd = None
+    if out is not None:
+        h, y, q8, scale, rstd = (out.get(n) for n in ("h", "y", "q8", "scale", "rstd"))
+    with _on(x, residual, weight, h, y, q8, scale, rstd):
+        if residual is not None and h is None:
+            h = torch.empty_like(x)
         if quant:
-            if res["q8"] is None:
-                res["q8"] = torch.empty((T, E), dtype=torch.float8_e4m3fn, device=x.device)
-            if res["scale"] is None:
-                res["scale"] = torch.empty(T, dtype=torch.float32, device=x.device)
-        elif res["y"] is None:
-            res["y"] = torch.empty_like(x)
-        if save_rstd and res["rstd"] is None:
-            res["rstd"] = torch.empty(T, dtype=torch.float32, device=x.device)
-        for n, t, shape in (("h", x.dtype, (T, E)), ("y", x.dtype, (T, E)),
-                            ("q8", torch.float8_e4m3fn, (T, E)), ("scale", torch.float32, (T,)),
-                            ("rstd", torch.float32, (T,))):
-            _dev(res[n], n, t)
-            _shape(res[n], n, *shape)
-        rc = lib.hstu_rmsnorm_fwd(dt, T, E, _ptr(x), _ptr(residual), _ptr(weight), float(eps),
-                                  _ptr(res["h"]), _ptr(res["y"]), _ptr(res["q8"]),
-                                  _ptr(res["scale"]), _ptr(res["rstd"]), _stream_ptr(stream))
+            if q8 is None:
+                q8 = torch.empty_like(x, dtype=_F8)
+            if scale is None:
+                scale = x.new_empty(T, dtype=_F32)
+        elif y is None:
+            y = torch.empty_like(x)
+        if save_rstd and rstd is None:
+            rstd = x.new_empty(T, dtype=_F32)
+        rc = lib.hstu_rmsnorm_fwd(dt, T, E, xp, rp, wp, eps, _arg(h, "h", x.dtype, T, E),
+                                  _arg(y, "y", x.dtype, T, E), _arg(q8, "q8", _F8, T, E),
+                                  _arg(scale, "scale", _F32, T), _arg(rstd, "rstd", _F32, T),
+                                  _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rmsnorm_fwd")
-    return res
+    return dict(h=h, y=y, q8=q8, scale=scale, rstd=rstd)
 
 
 def hstu_rmsnorm_bwd(dy, h, rstd, *, weight=None, d_residual=None, need_weight_grad=True,
@@ -474,32 +502,23 @@ def hstu_rmsnorm_bwd(dy, h, rstd, *, weight=None, d_residual=None, need_weight_g
     """Backward of hstu_rmsnorm_fwd from its h (x without a residual) and rstd.
     Returns (dx, d_weight fp32 [E] or None); dx is the residual's gradient too."""
     lib = load_library()
-    _dev(dy, "dy")
-    dt = _rows_dtype(dy)
-    _dev(h, "h", dy.dtype)
-    _dev(rstd, "rstd", torch.float32)
-    _dev(weight, "weight", torch.float32)
-    _dev(d_residual, "d_residual", dy.dtype)
-    if dy.dim() != 2:
-        raise ValueError("dy must be [T, E]")
+    dt = _rows_dtype(dy, "dy")
     T, E = dy.shape
-    _shape(h, "h", T, E)
-    _shape(rstd, "rstd", T)
-    _shape(weight, "weight", E)
-    _shape(d_residual, "d_residual", T, E)
+    args = (_arg(dy, "dy", dy.dtype), _arg(h, "h", dy.dtype, T, E), _arg(rstd, "rstd", _F32, T),
+            _arg(weight, "weight", _F32, E), _arg(d_residual, "d_residual", dy.dtype, T, E))
     with _on(dy, h, rstd, weight, d_residual, dx, workspace):
         if dx is None:
             dx = torch.empty_like(dy)
-        _dev(dx, "dx", dy.dtype)
-        _shape(dx, "dx", T, E)
-        dw = torch.empty(E, dtype=torch.float32, device=dy.device) if need_weight_grad else None
-        if need_weight_grad and workspace is None:
-            workspace = torch.empty(int(lib.hstu_rmsnorm_bwd_workspace_size(T, E)),
-                                    dtype=torch.uint8, device=dy.device)
-        rc = lib.hstu_rmsnorm_bwd(dt, T, E, _ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight),
-                                  _ptr(d_residual), _ptr(dx), _ptr(dw), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel(),
-                                  _stream_ptr(stream))
+        dw, wp, wn = None, None, 0
+        if need_weight_grad:
+            dw = dy.new_empty(E, dtype=_F32)
+            if workspace is None:
+                workspace = dy.new_empty(max(lib.hstu_rmsnorm_bwd_workspace_size(T, E), 256),
+                                         dtype=_U8)
+            workspace, wp, wn = _room(workspace, dy)
+        rc = lib.hstu_rmsnorm_bwd(dt, T, E, *args, _arg(dx, "dx", dy.dtype, T, E),
+                                  None if dw is None else dw.data_ptr(), wp, wn,
+                                  _stream_of(dy, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rmsnorm_bwd")
     return dx, dw
@@ -509,15 +528,14 @@ def hstu_quant_rows(x, *, stream=None):
     """Rows of x [T, E] (bf16 or fp32) as e4m3 bytes with one scale each.
     Returns (q8 [T, E] float8_e4m3fn, scale fp32 [T])."""
     lib = load_library()
-    _dev(x, "x")
-    dt = _rows_dtype(x)
-    if x.dim() != 2:
-        raise ValueError("x must be [T, E]")
+    dt = _rows_dtype(x, "x")
     T, E = x.shape
+    xp = _arg(x, "x", x.dtype)
     with _on(x):
-        q8 = torch.empty((T, E), dtype=torch.float8_e4m3fn, device=x.device)
-        scale = torch.empty(T, dtype=torch.float32, device=x.device)
-        rc = lib.hstu_quant_rows(dt, T, E, _ptr(x), _ptr(q8), _ptr(scale), _stream_ptr(stream))
+        q8 = torch.empty_like(x, dtype=_F8)
+        scale = x.new_empty(T, dtype=_F32)
+        rc = lib.hstu_quant_rows(dt, T, E, xp, q8.data_ptr(), scale.data_ptr(),
+                                 _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_quant_rows")
     return q8, scale
@@ -528,32 +546,22 @@ def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: 
     """UVQK projection act(x w^T + bias) of 8-bit rows: x8 [T, E], w8 [N, E]
     (float8_e4m3fn) with fp32 scales per row.  Returns the dict of hstu_uvqk_fwd."""
     lib = load_library()
-    for n, t in (("x8", x8), ("w8", w8)):
-        _dev(t, n, torch.float8_e4m3fn)
-    for n, t in (("x_scale", x_scale), ("w_scale", w_scale), ("bias", bias)):
-        _dev(t, n, torch.float32)
+    xp = _arg(x8, "x8", _F8)
     T, E = x8.shape
-    H = int(num_heads)
-    N = 2 * H * (int(d_qk) + int(d_v))
-    _shape(w8, "w8", N, E)
-    _shape(x_scale, "x_scale", T)
-    _shape(w_scale, "w_scale", N)
-    _shape(bias, "bias", N)
-    with _on(x8, x_scale, w8, w_scale, bias, workspace, *(out or {}).values()):
+    H, d_qk, d_v = int(num_heads), int(d_qk), int(d_v)
+    N = 2 * H * (d_qk + d_v)
+    args = (xp, _arg(x_scale, "x_scale", _F32, T), _arg(w8, "w8", _F8, N, E),
+            _arg(w_scale, "w_scale", _F32, N), _arg(bias, "bias", _F32, N))
+    with _on(x8, x_scale, w8, w_scale, bias, workspace):
         if out is None:
-            kw = dict(dtype=torch.bfloat16, device=x8.device)
-            out = dict(u=torch.empty((T, H * d_v), **kw), v=torch.empty((T, H, d_v), **kw),
-                       q=torch.empty((T, H, d_qk), **kw), k=torch.empty((T, H, d_qk), **kw))
-        for n, shape in (("u", (T, H * d_v)), ("v", (T, H, d_v)), ("q", (T, H, d_qk)),
-                         ("k", (T, H, d_qk))):
-            _dev(out[n], n, torch.bfloat16)
-            _shape(out[n], n, *shape)
-        if workspace is None:
-            workspace = _status_workspace(x8.device)
-        rc = lib.hstu_uvqk_fp8_fwd(T, E, H, int(d_qk), int(d_v), int(act), _ptr(x8),
-                                   _ptr(x_scale), _ptr(w8), _ptr(w_scale), _ptr(bias),
-                                   _ptr(out["u"]), _ptr(out["v"]), _ptr(out["q"]), _ptr(out["k"]),
-                                   _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+            new = lambda *s: x8.new_empty(s, dtype=_BF16)
+            out = dict(u=new(T, H * d_v), v=new(T, H, d_v), q=new(T, H, d_qk), k=new(T, H, d_qk))
+        u, v, q, k = out["u"], out["v"], out["q"], out["k"]
+        _on(x8, u, v, q, k)
+        workspace, wp, wn = _room(workspace, x8)
+        rc = lib.hstu_uvqk_fp8_fwd(T, E, H, d_qk, d_v, act, *args, _arg(u, "u", _BF16, T, H * d_v),
+                                   _arg(v, "v", _BF16, T, H, d_v), _arg(q, "q", _BF16, T, H, d_qk),
+                                   _arg(k, "k", _BF16, T, H, d_qk), wp, wn, _stream_of(x8, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_uvqk_fp8_fwd")
     return out
@@ -562,9 +570,9 @@ def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: 
 def hstu_pos_bucket_thresholds(num_buckets: int, max_exact: int, max_distance: int):
     """int32 CPU tensor [num_buckets - 1]: the smallest distance of each bucket
     from 1 on, exact up to max_exact, then logarithmic up to max_distance."""
-    out = torch.zeros(max(int(num_buckets) - 1, 1), dtype=torch.int32)
+    out = torch.zeros(max(int(num_buckets) - 1, 1), dtype=_I32)
     n = load_library().hstu_pos_bucket_thresholds(
-        _ptr(out) if 1 <= num_buckets <= 128 else None, int(num_buckets), int(max_exact),
+        out.data_ptr() if 1 <= num_buckets <= 128 else None, int(num_buckets), int(max_exact),
         int(max_distance))
     if n < 0:
         raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_pos_bucket_thresholds")
@@ -572,18 +580,17 @@ def hstu_pos_bucket_thresholds(num_buckets: int, max_exact: int, max_distance: i
 
 
 def _thresholds(thr, nb):
-    if not isinstance(thr, torch.Tensor) or thr.device.type != "cpu" or thr.dtype != torch.int32:
-        raise ValueError("thresholds must be an int32 CPU tensor")
-    thr = thr.contiguous()
-    _shape(thr, "thresholds", nb - 1)
-    return thr
+    if (not isinstance(thr, torch.Tensor) or thr.is_cuda or thr.dtype != _I32
+            or thr.shape != (nb - 1,) or not thr.is_contiguous()):
+        raise ValueError("thresholds must be a contiguous int32 CPU tensor [%d]" % (nb - 1))
+    return thr.data_ptr()
 
 
 def hstu_rab_bucket_fwd(table, length: int, thresholds, *, out=None, stream=None):
     """Position-bias table rab_pos [H, 2 length - 1] (fp32) from table [H, NB] and
     the buckets' thresholds (int32 CPU tensor [NB - 1])."""
     lib = load_library()
-    _dev(table, "table", torch.float32)
+    tp = _arg(table, "table", _F32)
     H, NB = table.shape
     thr = _thresholds(thresholds, NB)
     length = int(length)
@@ -591,11 +598,10 @@ def hstu_rab_bucket_fwd(table, length: int, thresholds, *, out=None, stream=None
         raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_rab_bucket_fwd")
     with _on(table, out):
         if out is None:
-            out = torch.empty((H, 2 * length - 1), dtype=torch.float32, device=table.device)
-        _dev(out, "out", torch.float32)
-        _shape(out, "out", H, 2 * length - 1)
-        rc = lib.hstu_rab_bucket_fwd(H, length, NB, _ptr(thr), _ptr(table), _ptr(out),
-                                     _stream_ptr(stream))
+            out = table.new_empty((H, 2 * length - 1))
+        rc = lib.hstu_rab_bucket_fwd(H, length, NB, thr, tp,
+                                     _arg(out, "out", _F32, H, 2 * length - 1),
+                                     _stream_of(table, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rab_bucket_fwd")
     return out
@@ -605,7 +611,7 @@ def hstu_rab_bucket_bwd(d_rab_pos, num_buckets: int, thresholds, *, out=None, st
     """Gradient [H, num_buckets] of hstu_rab_bucket_fwd's table from that of
     rab_pos [H, 2L - 1] (hstu_attn_bwd's d_rab_pos)."""
     lib = load_library()
-    _dev(d_rab_pos, "d_rab_pos", torch.float32)
+    gp = _arg(d_rab_pos, "d_rab_pos", _F32)
     H, W = d_rab_pos.shape
     if W % 2 != 1:
         raise ValueError("d_rab_pos must be [H, 2L - 1]")
@@ -613,11 +619,9 @@ def hstu_rab_bucket_bwd(d_rab_pos, num_buckets: int, thresholds, *, out=None, st
     thr = _thresholds(thresholds, NB)
     with _on(d_rab_pos, out):
         if out is None:
-            out = torch.empty((H, NB), dtype=torch.float32, device=d_rab_pos.device)
-        _dev(out, "out", torch.float32)
-        _shape(out, "out", H, NB)
-        rc = lib.hstu_rab_bucket_bwd(H, (W + 1) // 2, NB, _ptr(thr), _ptr(d_rab_pos), _ptr(out),
-                                     _stream_ptr(stream))
+            out = d_rab_pos.new_empty((H, NB))
+        rc = lib.hstu_rab_bucket_bwd(H, (W + 1) // 2, NB, thr, gp, _arg(out, "out", _F32, H, NB),
+                                     _stream_of(d_rab_pos, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rab_bucket_bwd")
     return out
@@ -627,22 +631,17 @@ def hstu_kv4_cache(cache_rows: int, num_heads: int, device):
     """An empty 4-bit cache: (k_codes, k_scales, v_codes, v_scales), codes uint8
     [cache_rows, H, 64], scales bf16 [cache_rows, H, 4]; it reads as zeros."""
     R, H = int(cache_rows), int(num_heads)
-    codes = lambda: torch.full((R, H, 64), 0x88, dtype=torch.uint8, device=device)
-    scales = lambda: torch.zeros((R, H, 4), dtype=torch.bfloat16, device=device)
+    codes = lambda: torch.full((R, H, 64), 0x88, dtype=_U8, device=device)
+    scales = lambda: torch.zeros((R, H, 4), dtype=_BF16, device=device)
     return codes(), scales(), codes(), scales()
 
 
-def _check_cache(cache):
+def _cache_args(cache):
+    """Rows, heads and the four addresses of a cache."""
     kc, ks, vc, vs = cache
-    for n, t in (("k_codes", kc), ("v_codes", vc)):
-        _dev(t, n, torch.uint8)
-    for n, t in (("k_scales", ks), ("v_scales", vs)):
-        _dev(t, n, torch.bfloat16)
     R, H = kc.shape[0], kc.shape[1]
-    for n, t, w in (("k_codes", kc, 64), ("k_scales", ks, 4), ("v_codes", vc, 64),
-                    ("v_scales", vs, 4)):
-        _shape(t, n, R, H, w)
-    return R, H
+    return R, H, (_arg(kc, "k_codes", _U8, R, H, 64), _arg(ks, "k_scales", _BF16, R, H, 4),
+                  _arg(vc, "v_codes", _U8, R, H, 64), _arg(vs, "v_scales", _BF16, R, H, 4))
 
 
 def hstu_kv4_pack(k, v, *, cache=None, rows=None, workspace=None, stream=None):
@@ -650,27 +649,23 @@ def hstu_kv4_pack(k, v, *, cache=None, rows=None, workspace=None, stream=None):
     ``rows`` (int32 [T], distinct, -1 skips), else to rows 0..T-1.  Without
     ``cache`` a new one of T rows.  Returns the cache."""
     lib = load_library()
-    for n, t in (("k", k), ("v", v)):
-        _dev(t, n, torch.bfloat16)
-    _dev(rows, "rows", torch.int32)
+    kp = _arg(k, "k", _BF16)
     T, H = k.shape[0], k.shape[1]
-    for n, t in (("k", k), ("v", v)):
-        _shape(t, n, T, H, 128)
-    _shape(rows, "rows", T)
+    kp, vp = _arg(k, "k", _BF16, T, H, 128), _arg(v, "v", _BF16, T, H, 128)
+    rp = _arg(rows, "rows", _I32, T)
     with _on(k, v, rows, workspace, *(cache or ())):
         if cache is None:
             if rows is not None:
                 raise ValueError("rows need a cache")
-            kw = dict(device=k.device)
-            cache = tuple(torch.empty((T, H, w), dtype=dt, **kw)
-                          for w, dt in ((64, torch.uint8), (4, torch.bfloat16)) * 2)
-        R, HC = _check_cache(cache)
+            cache = (k.new_empty((T, H, 64), dtype=_U8), k.new_empty((T, H, 4)),
+                     k.new_empty((T, H, 64), dtype=_U8), k.new_empty((T, H, 4)))
+        R, HC, ptrs = _cache_args(cache)
         if HC != H:
             raise ValueError("the cache has %d heads, k has %d" % (HC, H))
-        if workspace is None:
-            workspace = _status_workspace(k.device)
-        rc = lib.hstu_kv4_pack(T, H, _ptr(k), _ptr(v), _ptr(rows), R, *[_ptr(t) for t in cache],
-                               _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+        wp, wn = None, 0
+        if rows is not None or workspace is not None:
+            workspace, wp, wn = _room(workspace, k)
+        rc = lib.hstu_kv4_pack(T, H, kp, vp, rp, R, *ptrs, wp, wn, _stream_of(k, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_kv4_pack")
     return cache
@@ -680,22 +675,20 @@ def hstu_kv4_unpack(cache, *, rows=None, out=None, workspace=None, stream=None):
     """Keys and values [T, H, 128] (bf16) of a 4-bit cache's rows ``rows``
     (int32 [T]; a token of row -1 keeps what ``out`` holds), else of all rows."""
     lib = load_library()
-    _dev(rows, "rows", torch.int32)
-    R, H = _check_cache(cache)
+    R, H, ptrs = _cache_args(cache)
+    rp = _arg(rows, "rows", _I32)
     T = R if rows is None else rows.numel()
-    with _on(cache[0], *cache, rows, workspace, *(out or ())):
+    ref = cache[0]
+    with _on(ref, *cache, rows, workspace, *(out or ())):
         if out is None:
-            new = torch.empty if rows is None else torch.zeros
-            out = tuple(new((T, H, 128), dtype=torch.bfloat16, device=cache[0].device)
-                        for _ in range(2))
+            new = ref.new_empty if rows is None else ref.new_zeros
+            out = new((T, H, 128), dtype=_BF16), new((T, H, 128), dtype=_BF16)
         k, v = out
-        for n, t in (("k", k), ("v", v)):
-            _dev(t, n, torch.bfloat16)
-            _shape(t, n, T, H, 128)
-        if workspace is None:
-            workspace = _status_workspace(k.device)
-        rc = lib.hstu_kv4_unpack(T, H, *[_ptr(t) for t in cache], _ptr(rows), R, _ptr(k), _ptr(v),
-                                 _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+        kp, vp = _arg(k, "k", _BF16, T, H, 128), _arg(v, "v", _BF16, T, H, 128)
+        wp, wn = None, 0
+        if rows is not None or workspace is not None:
+            workspace, wp, wn = _room(workspace, ref)
+        rc = lib.hstu_kv4_unpack(T, H, *ptrs, rp, R, kp, vp, wp, wn, _stream_of(ref, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_kv4_unpack")
     return k, v
@@ -710,7 +703,7 @@ def hstu_cand_kv4_workspace(batch: int, num_heads: int, max_seq_len: int, total_
                                                         int(max_cands)))
     if n == 0:
         raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_cand_kv4_workspace_size")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return torch.zeros(n, dtype=_U8, device=device)
 
 
 def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets, max_cands: int, *,
@@ -723,61 +716,50 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
     offsets[B] (default: the timestamps' length, else the cache's rows, or, with
     first_rows, no bound).  Returns y [C, H*128]."""
     lib = load_library()
-    R, HC = _check_cache(cache)
-    for name, t in (("q", q), ("k", k), ("v", v), ("u", u)):
-        _dev(t, name, torch.bfloat16)
-    for name, t in (("offsets", offsets), ("cand_offsets", cand_offsets),
-                    ("first_rows", first_rows)):
-        _dev(t, name, torch.int32)
-    for name, t in (("timestamps", timestamps), ("cand_timestamps", cand_timestamps)):
-        _dev(t, name, torch.int64)
-    for name, t in (("rab_pos", rab_pos), ("rab_time", rab_time), ("ln_weight", ln_weight),
-                    ("ln_bias", ln_bias)):
-        _dev(t, name, torch.float32)
+    R, HC, ptrs = _cache_args(cache)
+    qp = _arg(q, "q", _BF16)
     C, H, _ = q.shape
     B = offsets.numel() - 1
     if H != HC:
         raise ValueError("the cache has %d heads, q has %d" % (HC, H))
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _shape(t, name, C, H, 128)
-    _shape(u, "u", C, H * 128)
-    _shape(cand_offsets, "cand_offsets", B + 1)
-    _shape(first_rows, "first_rows", B)
-    _shape(cand_timestamps, "cand_timestamps", C)
-    _shape(ln_weight, "ln_weight", H * 128)
-    _shape(ln_bias, "ln_bias", H * 128)
-    for name, t in (("rab_pos", rab_pos), ("rab_time", rab_time)):
-        if t is not None and (t.dim() != 2 or t.shape[0] != H):
-            raise ValueError("%s must have %d rows" % (name, H))
-    if rab_pos is not None and rab_pos.shape[1] % 2 != 1:
+    if rab_pos is not None and (rab_pos.dim() != 2 or rab_pos.shape[1] % 2 != 1):
         raise ValueError("rab_pos must be [H, 2L - 1]")
+    if timestamps is not None and timestamps.dim() != 1:
+        raise ValueError("timestamps must be [T]")
+    W = 0 if rab_pos is None else rab_pos.shape[1]
+    NB = 0 if rab_time is None else rab_time.shape[-1]
     limit = (timestamps.numel() if timestamps is not None else
              R if first_rows is None else 2 ** 31 - 1)
+    if offsets_host is not None:
+        total_tokens = int(offsets_host[-1])
     if total_tokens is None:
         total_tokens = limit
     elif timestamps is not None and total_tokens > limit:
         raise ValueError("total_tokens exceeds the timestamps' length")
     with _on(q, *cache, offsets, k, v, u, cand_offsets, first_rows, timestamps, cand_timestamps,
              rab_pos, rab_time, ln_weight, ln_bias, y, workspace):
-        p = make_problem(q, v, offsets, max_seq_len, timestamps, rab_pos, rab_time, norm_len, eps,
-                         None, ln_weight, ln_bias)
-        p.total_tokens = int(total_tokens)
-        if timestamps is not None and rab_time is not None and timestamps.numel() == 0:
-            p.timestamps = rab_time.data_ptr()   # nothing to read; an empty tensor has no address
-        if offsets_host is not None:
-            p.total_tokens = int(offsets_host[-1])
-            p.offsets_host = offsets_host.data_ptr()
+        p = hstu_problem_t(HSTU_BF16, B, total_tokens, max_seq_len, H, 128, 128,
+                           _arg(offsets, "offsets", _I32, B + 1),
+                           None if offsets_host is None else offsets_host.data_ptr(),
+                           _arg(timestamps, "timestamps", _I64),
+                           _arg(rab_pos, "rab_pos", _F32, H, W), (W + 1) // 2,
+                           _arg(rab_time, "rab_time", _F32, H, NB), NB, norm_len, eps,
+                           _arg(ln_weight, "ln_weight", _F32, H * 128),
+                           _arg(ln_bias, "ln_bias", _F32, H * 128))
+        if rab_time is not None and timestamps is not None and total_tokens == 0:
+            p.timestamps = p.rab_time   # nothing to read; an empty tensor has no address
         if y is None:
-            y = torch.empty((C, H * 128), dtype=q.dtype, device=q.device)
-        _dev(y, "y", q.dtype)
-        _shape(y, "y", C, H * 128)
+            y = torch.empty_like(u)
         if workspace is None:
             workspace = hstu_cand_kv4_workspace(B, H, max_seq_len, C, max_cands, q.device)
-        rc = lib.hstu_cand_kv4_fwd(ctypes.byref(p), *[_ptr(t) for t in cache], R,
-                                   _ptr(first_rows), _ptr(cand_offsets), C, int(max_cands),
-                                   _ptr(cand_timestamps), _ptr(q), _ptr(k), _ptr(v), _ptr(u),
-                                   _ptr(y), _ptr(workspace), workspace.numel(),
-                                   _stream_ptr(stream))
+        workspace, wp, wn = _room(workspace, q)
+        rc = lib.hstu_cand_kv4_fwd(
+            ctypes.byref(p), *ptrs, R, _arg(first_rows, "first_rows", _I32, B),
+            _arg(cand_offsets, "cand_offsets", _I32, B + 1), C, max_cands,
+            _arg(cand_timestamps, "cand_timestamps", _I64, C), _arg(q, "q", _BF16, C, H, 128),
+            _arg(k, "k", _BF16, C, H, 128), _arg(v, "v", _BF16, C, H, 128),
+            _arg(u, "u", _BF16, C, H * 128), _arg(y, "y", _BF16, C, H * 128), wp, wn,
+            _stream_of(q, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_cand_kv4_fwd")
     return y

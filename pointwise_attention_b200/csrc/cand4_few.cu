@@ -26,6 +26,8 @@
 // applies the LayerNorm and the gate.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "bounds.cuh"
 #include "internal.h"
 #include "kv4.cuh"
@@ -397,15 +399,11 @@ cudaError_t launch_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_su
 template <bool POS, bool TIME>
 cudaError_t launch_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(a.B) * cut.cgroups * cut.splits * cut.hgroups;
-  if (grid > 0) {
-    if (cut.nt == 1)
-      hstu_cand4_few<1, POS, TIME><<<grid, kThreads, 0, stream>>>(a, cut);
-    else
-      hstu_cand4_few<2, POS, TIME><<<grid, kThreads, 0, stream>>>(a, cut);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-  }
-  return launch_finish<POS, TIME>(a, cut, grid > 0, stream);
+  if (cut.nt == 1)
+    hstu_cand4_few<1, POS, TIME><<<grid, kThreads, 0, stream>>>(a, cut);
+  else
+    hstu_cand4_few<2, POS, TIME><<<grid, kThreads, 0, stream>>>(a, cut);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -414,15 +412,35 @@ cudaError_t launch_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t str
 // 16-key blocks per warp, at most kMaxChunk.
 constexpr int64_t kCtas = 4 * 148;
 
+// More candidates per user than this take the tcgen05 kernel.
+constexpr int kFewMax = 16;
+
 Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands) {
   Cand4Cut c;
+  c.many = max_cands > kFewMax;
+  if (c.many) {
+    c.heads = 1;
+    c.parts = 1;
+    c.hgroups = H;
+    c.nt = 0;
+    c.cgroups = static_cast<int>((static_cast<int64_t>(max_cands) + 255) / 256);
+    // one CTA walks a whole history where there are CTAs enough; otherwise
+    // histories are cut so that there are about two a SM
+    const int64_t groups = static_cast<int64_t>(B) * H * c.cgroups;
+    const int64_t want = groups > 2 * 148 ? 1 : (2 * 148 + groups - 1) / (groups > 0 ? groups : 1);
+    int64_t chunk = ((max_seq_len + want - 1) / want + 127) / 128 * 128;
+    if (chunk < 256) chunk = 256;
+    c.chunk = static_cast<int>(chunk);
+    c.splits = static_cast<int>((max_seq_len + chunk - 1) / chunk);
+    return c;
+  }
   c.heads = H < kWarps ? H : kWarps;
   c.parts = kWarps / c.heads;
   c.hgroups = (H + kWarps - 1) / kWarps;
   c.nt = max_cands <= 8 ? 1 : 2;
   c.cgroups = static_cast<int>((static_cast<int64_t>(max_cands) + 8 * c.nt - 1) / (8 * c.nt));
   const int64_t step = 16 * c.parts;
-  const int64_t groups = static_cast<int64_t>(B) * c.hgroups * c.cgroups;   // below 2^31 2^4
+  const int64_t groups = static_cast<int64_t>(B) * c.hgroups * c.cgroups;
   int64_t chunk = groups > kCtas ? kMaxChunk : (groups * max_seq_len / kCtas + step - 1) / step * step;
   const int64_t most = kMaxChunk / step * step;
   chunk = chunk < 2 * step ? 2 * step : chunk > most ? most : chunk;
@@ -431,21 +449,34 @@ Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands) {
   return c;
 }
 
-// splits <= max_seq_len / (2 step) + 1 always, and splits <= kCtas / groups + 1
-// where the chunk is between its limits; C <= 16 groups / hgroups candidates
-// then make at most 16 kCtas + C rows a part, and max_seq_len / most + 1 splits
-// at the upper limit.
-size_t cand4_part_rows(int H, int max_seq_len, int C) {
-  const int parts = H < kWarps ? kWarps / H : 1;
+// Few candidates: splits <= max_seq_len / (2 step) + 1 always, and splits <=
+// kCtas / groups + 1 where the chunk is between its limits; C <= 16 groups /
+// hgroups candidates then make at most 16 kCtas + C rows a part, and
+// max_seq_len / most + 1 splits at the upper limit.  Many: splits <=
+// max_seq_len / 256 + 1, and splits <= 296 / groups + 1 with C <= 256 groups / H.
+size_t cand4_part_rows(int H, int max_seq_len, int C, int max_cands) {
+  const int64_t parts = H < kWarps ? kWarps / H : 1;
   const int64_t step = 16 * parts, most = kMaxChunk / step * step;
   const int64_t c = C, n = max_seq_len;
-  const int64_t fine = c * (n / (2 * step) + 1);
-  const int64_t coarse = 16 * kCtas + c * (n / most + 2);
-  return static_cast<size_t>(parts) * static_cast<size_t>(fine < coarse ? fine : coarse);
+  const int64_t few = parts * std::min(c * (n / (2 * step) + 1), 16 * kCtas + c * (n / most + 2));
+  const int64_t many = std::min(c * (n / 256 + 1), c + 2 * 148 * 256 / H + 1);
+  return static_cast<size_t>(max_cands > kFewMax ? std::max(few, many) : few);
+}
+
+size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands) {
+  return max_cands > kFewMax ? (static_cast<size_t>(max_seq_len) + 127) / 128 * 16 * C : 0;
+}
+
+cudaError_t launch_cand4_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_sums,
+                                cudaStream_t stream) {
+  const bool pos = a.rab_pos != nullptr, time = a.rab_time != nullptr;
+  if (pos && time) return launch_finish<true, true>(a, cut, after_sums, stream);
+  if (pos) return launch_finish<true, false>(a, cut, after_sums, stream);
+  if (time) return launch_finish<false, true>(a, cut, after_sums, stream);
+  return launch_finish<false, false>(a, cut, after_sums, stream);
 }
 
 cudaError_t launch_cand4_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t stream) {
-  if (a.B == 0 || a.C == 0) return cudaSuccess;
   const bool pos = a.rab_pos != nullptr, time = a.rab_time != nullptr;
   if (pos && time) return launch_few<true, true>(a, cut, stream);
   if (pos) return launch_few<true, false>(a, cut, stream);

@@ -63,7 +63,7 @@ const Thresholds& thresholds() {
   return t;
 }
 
-void fill_bucket_table(BucketTable* bt, int nb) {
+void make_bucket_table(BucketTable* bt, int nb) {
   const Thresholds& t = thresholds();
   for (int k = 0; k < kThrLen; ++k)
     bt->thr[k] = (k < nb && k < kMaxBuckets) ? t.thr[k] : 0x7FFFFFFFFFFFFFFFll;
@@ -80,6 +80,14 @@ void fill_bucket_table(BucketTable* bt, int nb) {
     auto t = [&](int i) { return k + i < kMaxBuckets ? bt->thr32[k + i] : 0xFFFFFFFFu; };
     bt->oct[e] = make_uint4(static_cast<unsigned>(k), t(1), t(2), t(3));
   }
+}
+
+// The table of nb buckets, made once per nb (it depends on nothing else): making it takes a few microseconds, copying it a fraction of one.
+void fill_bucket_table(BucketTable* bt, int nb) {
+  static BucketTable tables[kMaxBuckets + 1];
+  static std::once_flag once[kMaxBuckets + 1];
+  std::call_once(once[nb], [nb] { make_bucket_table(&tables[nb], nb); });
+  *bt = tables[nb];
 }
 
 // ---------------------------------------------------------- TMA tensor maps
@@ -717,8 +725,11 @@ size_t hstu_cand_kv4_workspace_size(int32_t batch, int32_t num_heads, int32_t ma
   if (batch < 0 || num_heads < 1 || num_heads > 16 || max_seq_len < 0 || total_cands < 0 ||
       max_cands < 0)
     return 0;
-  return kStatusBytes + align_up(cand4_part_rows(num_heads, max_seq_len, total_cands) *
-                                 static_cast<size_t>(num_heads) * 512);
+  // [status][sums][time plans]
+  return kStatusBytes +
+         align_up(cand4_part_rows(num_heads, max_seq_len, total_cands, max_cands) *
+                  static_cast<size_t>(num_heads) * 512) +
+         align_up(cand4_plan_bytes(max_seq_len, total_cands, max_cands));
 }
 
 hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, const void* k_scales,
@@ -755,6 +766,8 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
   if (static_cast<double>(p->batch) * cut.cgroups * cut.splits * cut.hgroups > 2147483647.0 ||
       static_cast<double>(p->batch) * max_cands > 2147483647.0)
     return HSTU_ERR_UNSUPPORTED;
+  // the plan pass: 8 blocks of 32 keys per CTA along a grid's y
+  if (cut.many && p->rab_time && p->max_seq_len > 65535 * 256) return HSTU_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kAlign) != 0 ||
       workspace_bytes < hstu_cand_kv4_workspace_size(p->batch, p->num_heads, p->max_seq_len,
                                                      total_cands, max_cands))
@@ -792,8 +805,42 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
   a.eps = p->ln_eps;
   a.chunk = cut.chunk;
   a.splits = cut.splits;
-  fill_bucket_table(&a.bt, p->rab_time ? p->num_time_buckets : 1);
-  const cudaError_t err = launch_cand4_few(a, cut, static_cast<cudaStream_t>(stream));
+  if (p->rab_time) fill_bucket_table(&a.bt, p->num_time_buckets);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const bool hist = p->total_tokens > 0 && p->max_seq_len > 0;
+  cudaError_t err = cudaSuccess;
+  if (hist && cut.many) {
+    CUtensorMap tq;
+    if (!make_map_3d(&tq, q, total_cands, p->num_heads, 128)) return HSTU_ERR_CUDA;
+    if (p->rab_time) {
+      uint32_t* plan = reinterpret_cast<uint32_t*>(
+          static_cast<uint8_t*>(workspace) + kStatusBytes +
+          align_up(cand4_part_rows(p->num_heads, p->max_seq_len, total_cands, max_cands) *
+                   static_cast<size_t>(p->num_heads) * 512));
+      a.plan = plan;
+      CandArgs pa;
+      std::memset(&pa, 0, sizeof(pa));
+      pa.offsets = a.offsets;
+      pa.cand_offsets = cand_offsets;
+      pa.timestamps = a.timestamps;
+      pa.cand_ts = cand_timestamps;
+      pa.plan = plan;
+      pa.plan_j = 4 * ((p->max_seq_len + 127) / 128);
+      pa.status = a.status;
+      pa.B = a.B;
+      pa.T = a.T;
+      pa.C = a.C;
+      pa.H = a.H;
+      pa.max_tiles = (max_cands + 127) / 128;
+      pa.max_seq_len = a.max_seq_len;
+      pa.bt = a.bt;
+      err = launch_cand_plans(pa, cs);   // the time-plan shapes, once for all heads
+    }
+    if (err == cudaSuccess) err = launch_cand4_sm100(a, tq, cs);
+  } else if (hist) {
+    err = launch_cand4_few(a, cut, cs);
+  }
+  if (err == cudaSuccess) err = launch_cand4_finish(a, cut, hist, cs);
   return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 

@@ -226,8 +226,9 @@ struct Cand4Args {
   const float* ln_weight;        // [H*128] or nullptr
   const float* ln_bias;
   // workspace: sums over the history, [slices][C][H*128] fp32; a slice is the
-  // part of a history that one warp walks
+  // part of a history that one warp (many candidates: one CTA) walks
   float* part;
+  const uint32_t* plan;          // many candidates, with a time table: CandArgs::plan
   int* status;
   int B, T, C, H, R;
   int max_seq_len, max_cands;
@@ -237,19 +238,22 @@ struct Cand4Args {
   BucketTable bt;
 };
 
-// How the few-candidate kernel cuts a problem (sizes alone decide).
+// How a problem is cut (sizes alone decide).
 struct Cand4Cut {
-  int heads;     // heads of a CTA: one warp each, times
-  int parts;     // warps that share a head's keys
+  int many;      // the kernel for many candidates: 256 of them, a head a CTA
+  int heads;     // few: heads of a CTA, one warp each, times
+  int parts;     // few: warps that share a head's keys (many: 1)
   int hgroups;   // CTAs along the heads
-  int nt;        // groups of 8 candidates of a CTA
+  int nt;        // few: groups of 8 candidates of a CTA
   int cgroups;   // CTAs along a user's candidates
-  int chunk, splits;
+  int chunk, splits;   // history keys per CTA, CTAs along the longest history
 };
 Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands);
 // Rows (of H*128 fp32) that hold the sums of every cut with H heads, histories
-// of at most max_seq_len and at most C candidates: grows with each of them.
-size_t cand4_part_rows(int H, int max_seq_len, int C);
+// of at most max_seq_len and at most C candidates, max_cands a user, and the
+// bytes of the many-candidate kernel's time plans: both grow with each of them.
+size_t cand4_part_rows(int H, int max_seq_len, int C, int max_cands);
+size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands);
 
 // The synchronous argument checks of hstu_attn_bwd (all but the workspace's).
 hstu_status_t check_bwd_args(const hstu_problem_t* p, const void* dy, const void* q,
@@ -269,6 +273,9 @@ cudaError_t launch_bwd_pre_bf16(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_cand_sm100(const CandArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_cand4_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t stream);
+cudaError_t launch_cand4_sm100(const Cand4Args& a, const CUtensorMap& tq, cudaStream_t stream);
+cudaError_t launch_cand4_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_sums,
+                                cudaStream_t stream);
 cudaError_t launch_uvqk_sm100(const ProjArgs& a, const CUtensorMap& tx, const CUtensorMap& tw,
                               cudaStream_t stream);
 int uvqk_fp8_cols(int T, int N);   // columns of a tile of the 8-bit projection

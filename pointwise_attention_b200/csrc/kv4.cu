@@ -124,7 +124,9 @@ hstu_status_t run(bool pack, int32_t T, int32_t H, int32_t cache_rows, const int
   // one thread per word, 256 a block, blocks in grid x
   const int64_t units = 16ll * T * H;
   if (H > 65536 || units > 0x7FFFFFFFll * kThreads) return HSTU_ERR_UNSUPPORTED;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 || workspace_bytes < 256)
+  // only the cache rows given by index can be found wrong on the device
+  if ((rows || workspace) && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
+                              workspace_bytes < 256))
     return HSTU_ERR_WORKSPACE;
   if (T == 0) return HSTU_OK;
   Kv4Args a;

@@ -106,7 +106,7 @@ UNKV = dict(T=4, H=2, p_kc=FAKE, p_ks=FAKE, p_vc=FAKE, p_vs=FAKE, p_rows=None, R
 @pytest.mark.parametrize("change,want", [
     (dict(T=-1), INV), (dict(H=0), INV), (dict(R=-1), INV), (dict(R=3), INV),
     (dict(p_k=None), INV), (dict(p_vc=None), INV), (dict(p_ks=FAKE + 8), INV),
-    (dict(p_rows=FAKE + 2), INV), (dict(H=65537), UNS), (dict(p_ws=None), WS),
+    (dict(p_rows=FAKE + 2), INV), (dict(H=65537), UNS), (dict(p_rows=FAKE, p_ws=None), WS),
     (dict(p_ws=FAKE + 128), WS), (dict(bytes=255), WS)])
 def test_kv4_refusals(pa, which, change, want):
     lib = pa.load_library()
