@@ -6,13 +6,14 @@
 // A CTA takes (user, 256 candidates, head, up to `chunk` keys): two tiles of
 // 128 candidates share every decoded tile of 128 keys and values, which halves
 // the decoding, and fill TMEM: S0, S1, O0, O1 at 128 columns each.
-//   warps 0..3    decode: codes and scales from the cache (one tile ahead in
-//                 registers) to bf16 in the 128-byte-swizzled layout of the
-//                 MMA operands, two stages each of K and V; the keys' position
-//                 bias and timestamps beside them
-//   warps 4..19   epilogue, eight warps per candidate tile: half bias and SiLU
-//                 in fp32, P (bf16, its one rounding) over S in TMEM; then O
-//   warp 20       TMEM, the candidates' Q by TMA, and every MMA: while one
+//   warps 0..3    decode K (warps 4..7: V): codes and scales from the cache, a
+//                 tile ahead in registers, to bf16 in the 128-byte-swizzled
+//                 layout of the MMA operands, two stages each; the keys'
+//                 position bias and timestamps beside K
+//   warps 8..15   epilogue, four per candidate tile, a row (TMEM lane) per
+//                 thread: half bias and SiLU in fp32, P (bf16, its one
+//                 rounding) over S in TMEM; then O
+//   warp 16       TMEM, the candidates' Q by TMA, and every MMA: while one
 //                 tile's scores are in the epilogue, the tensor core works for
 //                 the other
 // SiLU(x) = h (1 + tanh h), h = x / 2, with tanh.approx.f32 (one special
@@ -32,9 +33,11 @@
 namespace hstu {
 namespace {
 
-constexpr int kDecWarps = 4;
-constexpr int kEpiWarps = 16;
-constexpr int kThreads = 32 * (kDecWarps + kEpiWarps + 1);
+constexpr int kDecWarps = 4;               // of K, and as many of V
+constexpr int kEpi0 = 2 * kDecWarps;       // first epilogue warp
+constexpr int kEpiWarps = 8;
+constexpr int kMmaWarp = kEpi0 + kEpiWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kHalf = 16384;               // 128 rows x 64 bf16
 constexpr int kTile = 2 * kHalf;           // 128 x 128 bf16
 constexpr int kRing = 4;                   // key metadata of this many tiles
@@ -89,36 +92,39 @@ __device__ __forceinline__ bool flagged(bool ok, int* status) {
 }
 
 // P pairs of one 32-key block from its scores: h = S / 2 + half bias, h + h tanh h.
+// tv, ts: the plan's half biases and split columns (tile_math.cuh).
 template <bool POS, int TB>
 __device__ __forceinline__ void p_block(const uint32_t (&sv)[32], const float* pos,
                                         const uint32_t* ts32, const float (&tv)[4], const int (&ts)[3],
                                         uint32_t my32, const Tab& tab, uint32_t (&packed)[16]) {
+  const uint64_t half2 = pack_f32x2(0.5f, 0.5f), tc2 = pack_f32x2(tv[0], tv[0]);
 #pragma unroll
-  for (int c4 = 0; c4 < 8; ++c4) {
-    float4 p4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (POS) p4 = *reinterpret_cast<const float4*>(pos + 4 * c4);
-    const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
-    float y[4];
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t s2 = pack_f32x2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+    uint64_t h2;
+    if (POS) {
+      h2 = ffma2(s2, half2, *reinterpret_cast<const uint64_t*>(pos + 2 * i));
+      if (TB == TB_CONST) h2 = fadd2(h2, tc2);
+    } else {
+      h2 = ffma2(s2, half2, TB == TB_CONST ? tc2 : 0ull);
+    }
+    if (TB == TB_SPLIT || TB == TB_MULTI || TB == TB_GEN32) {
+      float b[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int c = 4 * c4 + e;
-      float h = __uint_as_float(sv[c]);
-      if (TB == TB_CONST && !POS) {
-        h = fmaf(h, 0.5f, tv[0]);
-      } else {
-        h = POS ? fmaf(h, 0.5f, pv[e]) : 0.5f * h;
-        if (TB == TB_CONST) h += tv[0];
-        if (TB == TB_SPLIT) h += c < ts[0] ? tv[0] : tv[1];
-        if (TB == TB_MULTI) h += c >= ts[2] ? tv[3] : c >= ts[1] ? tv[2] : c >= ts[0] ? tv[1] : tv[0];
+      for (int e = 0; e < 2; ++e) {
+        const int c = 2 * i + e;
+        if (TB == TB_SPLIT) b[e] = c < ts[0] ? tv[0] : tv[1];
+        if (TB == TB_MULTI) b[e] = c >= ts[2] ? tv[3] : c >= ts[1] ? tv[2] : c >= ts[0] ? tv[1] : tv[0];
         if (TB == TB_GEN32) {
           const int d = static_cast<int>(ts32[c] - my32);
-          h += tab.rabt()[bucket32(static_cast<uint32_t>(d < 0 ? -d : d), tab.oct())];
+          b[e] = tab.rabt()[bucket32(static_cast<uint32_t>(d < 0 ? -d : d), tab.oct())];
         }
       }
-      y[e] = fmaf(h, tanh_approx(h), h);
+      h2 = fadd2(h2, pack_f32x2(b[0], b[1]));
     }
-    packed[2 * c4] = pack_bf16x2(y[0], y[1]);
-    packed[2 * c4 + 1] = pack_bf16x2(y[2], y[3]);
+    const float2 h = unpack_f32x2(h2);
+    const float2 y = unpack_f32x2(ffma2(h2, pack_f32x2(tanh_approx(h.x), tanh_approx(h.y)), h2));
+    packed[i] = pack_bf16x2(y.x, y.y);
   }
 }
 
@@ -152,7 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (broadcast, so that the compiler knows the roles' branches to be warp-uniform)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   auto bar = [&](int i) { return sbase + kOffBar + 8u * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_VFULL + i), kDecWarps);
       mbar_init(bar(B_VEMPTY + i), 1);
       mbar_init(bar(B_SFULL + i), 1);
-      mbar_init(bar(B_PFULL + i), kEpiWarps / 2);
+      mbar_init(bar(B_PFULL + i), kEpiWarps / 2);   // the tile's epilogue warps
       mbar_init(bar(B_PVDONE + i), 1);
     }
     mbar_init(bar(B_OFULL), 1);
@@ -236,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = threadIdx.x; i < kMaxBuckets; i += kThreads)
       reinterpret_cast<unsigned*>(smem + kOffThr32)[i] = a.bt.thr32[i];
   }
-  if (warp == kDecWarps + kEpiWarps) {
+  if (warp == kMmaWarp) {
     tmem_alloc(sbase + kOffMisc, 512);
     tmem_relinquish();
     if (lane == 0) tma_prefetch_desc(&tm_q);
@@ -246,159 +254,158 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  if (warp < kDecWarps) {
+  if (warp < kEpi0) {
     // ------------------------------------------------------------ decode
-    // lane (row, t): the row's dims 32t..32t+31; rows warp 8 + 32 i + row
-    const int t = lane & 3, row = 8 * warp + (lane >> 2);
+    // lane (row, t): the row's dims 32t..32t+31; rows 8 w + 32 i + row of the tile
+    const bool is_k = warp < kDecWarps;
+    const int w = warp & (kDecWarps - 1), t = lane & 3, row = 8 * w + (lane >> 2);
+    const uint8_t* codes = is_k ? a.k_codes : a.v_codes;
+    const uint16_t* scales = is_k ? a.k_scales : a.v_scales;
+    const uint32_t dst = sbase + (is_k ? kOffK : kOffV);
+    const int b_full = is_k ? B_KFULL : B_VFULL, b_empty = is_k ? B_KEMPTY : B_VEMPTY;
     const float* rpos =
         POS ? a.rab_pos + static_cast<size_t>(h) * (2 * static_cast<size_t>(a.L) - 1) + (a.L - 1) : nullptr;
-    struct Regs {
-      uint4 c[4];
-      uint32_t s[4];
-    } k, v;
+    uint4 c[4];
+    uint32_t sc[4];
     float pos = 0.f;
     uint32_t ts = 0;
-    auto load = [&](const uint8_t* codes, const uint16_t* scales, int n, Regs& r) {
+    auto load = [&](int n) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = 128 * n + 32 * i + row;
-        r.c[i] = make_uint4(0u, 0u, 0u, 0u);      // keys past the CTA's decode to zeros
-        r.s[i] = 0u;
+        c[i] = make_uint4(0u, 0u, 0u, 0u);      // keys past the CTA's decode to zeros
+        sc[i] = 0u;
         if (key < keys) {
           const size_t at =
               static_cast<size_t>(checked(a.status, r0 + key0 + key, a.R, BS_CAND4_KEY)) * a.H + h;
-          r.c[i] = __ldg(reinterpret_cast<const uint4*>(codes + at * 64) + t);
-          r.s[i] = __ldg(scales + at * 4 + t);
+          c[i] = __ldg(reinterpret_cast<const uint4*>(codes + at * 64) + t);
+          sc[i] = __ldg(scales + at * 4 + t);
         }
       }
+      if (is_k) {
+        const int key = 128 * n + 32 * w + lane;
+        if (POS) pos = key < keys ? __ldg(rpos + (nb - key0 - key)) : 0.f;
+        if (TIME)
+          ts = static_cast<uint32_t>(__ldg(
+              a.timestamps + checked(a.status, s + key0 + min(key, keys - 1), a.T, BS_CAND4_TS)));
+      }
     };
-    auto load_meta = [&](int n) {
-      const int key = 128 * n + 32 * warp + lane;
-      const bool in = key < keys;
-      if (POS) pos = in ? 0.5f * __ldg(rpos + (nb - key0 - key)) : 0.f;
-      if (TIME)
-        ts = static_cast<uint32_t>(__ldg(
-            a.timestamps + checked(a.status, s + key0 + min(key, keys - 1), a.T, BS_CAND4_TS)));
-    };
-    load(a.k_codes, a.k_scales, 0, k);
-    load_meta(0);
-    load(a.v_codes, a.v_scales, 0, v);
+    load(0);
     bool ok = true;
     for (int n = 0; n < nt; ++n) {
-      const int st = n & 1, use = n >> 1;
-      if (use > 0) ok = flagged(mbar_wait(bar(B_KEMPTY + st), (use - 1) & 1, abort_flag), a.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      const int st = n & 1, use = n >> 1, slot = n & (kRing - 1);
+      if (use > 0) ok = flagged(mbar_wait(bar(b_empty + st), (use - 1) & 1, abort_flag), a.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        decode_group(sbase + kOffK + st * kTile, row + 32 * i, t, k.c[i], k.s[i]);
-      // this slot's last readers finished tile n - kRing before S of tile n - 2
-      // could be issued, which the wait above saw completed
-      if (POS) reinterpret_cast<float*>(smem + kOffPos)[(n & (kRing - 1)) * 128 + 32 * warp + lane] = pos;
-      if (TIME) reinterpret_cast<uint32_t*>(smem + kOffTs)[(n & (kRing - 1)) * 128 + 32 * warp + lane] = ts;
+      for (int i = 0; i < 4; ++i) decode_group(dst + st * kTile, row + 32 * i, t, c[i], sc[i]);
+      if (is_k) {
+        // the slot's last readers finished tile n - kRing before S of tile n - 2
+        // could be issued, which the wait above saw completed
+        if (POS) reinterpret_cast<float*>(smem + kOffPos)[slot * 128 + 32 * w + lane] = 0.5f * pos;
+        if (TIME) reinterpret_cast<uint32_t*>(smem + kOffTs)[slot * 128 + 32 * w + lane] = ts;
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(B_KFULL + st));
-        mbar_arrive(bar(B_META + (n & (kRing - 1))));
+        mbar_arrive(bar(b_full + st));
+        if (is_k) mbar_arrive(bar(B_META + slot));
       }
-      if (n + 1 < nt) {
-        load(a.k_codes, a.k_scales, n + 1, k);
-        load_meta(n + 1);
-      }
-      if (use > 0) ok = flagged(mbar_wait(bar(B_VEMPTY + st), (use - 1) & 1, abort_flag), a.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        decode_group(sbase + kOffV + st * kTile, row + 32 * i, t, v.c[i], v.s[i]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_VFULL + st));
-      if (n + 1 < nt) load(a.v_codes, a.v_scales, n + 1, v);
+      if (n + 1 < nt) load(n + 1);
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp == kDecWarps + kEpiWarps) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ Q and the MMAs
-    if (lane == 0) {
+    // the whole warp walks the schedule; one lane issues
+    if (elect_one()) {
       for (int g = 0; g < tiles; ++g) {
         const int qrow = checked(a.status, cand0 + 128 * g, a.C, BS_CAND4_ROW);
         mbar_arrive_expect_tx(bar(B_QFULL + g), kTile);
         tma_load_3d(sbase + kOffQ + g * kTile, &tm_q, bar(B_QFULL + g), 0, h, qrow);
         tma_load_3d(sbase + kOffQ + g * kTile + kHalf, &tm_q, bar(B_QFULL + g), 64, h, qrow);
       }
-      bool ok = true;
-      auto wait = [&](int i, int parity) {
-        ok = ok && flagged(mbar_wait(bar(i), parity & 1, abort_flag), a.status);
-      };
-      // S of candidate tile g and key tile n; its columns hold P of tile n - 1
-      // until that tile's P V is done
-      auto issue_s = [&](int g, int n) {
-        const int st = n & 1;
-        if (n == 0) wait(B_QFULL + g, 0);
-        wait(B_KFULL + st, n >> 1);
-        if (n > 0) wait(B_PVDONE + g, n - 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t qa = sbase + kOffQ + g * kTile, ka = sbase + kOffK + st * kTile;
+    }
+    __syncwarp();
+    bool ok = true;
+    auto wait = [&](int i, int parity) {
+      if (ok)
+        ok = __all_sync(0xffffffffu,
+                        flagged(mbar_wait(bar(i), parity & 1, abort_flag), a.status));
+    };
+    // S of candidate tile g and key tile n; its columns hold P of tile n - 1
+    // until that tile's P V is done
+    auto issue_s = [&](int g, int n) {
+      const int st = n & 1;
+      if (n == 0) wait(B_QFULL + g, 0);
+      wait(B_KFULL + st, n >> 1);
+      if (n > 0) wait(B_PVDONE + g, n - 1);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t qd = sw128_desc(sbase + kOffQ + g * kTile, 16, 1024);
+        const uint64_t kd = sw128_desc(sbase + kOffK + st * kTile, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-          mma_ss(tmem + 128u * g, sw128_desc(qa + off, 16, 1024), sw128_desc(ka + off, 16, 1024),
-                 kIdescS, ks > 0 ? 1u : 0u);
+          const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+          mma_ss(tmem + 128u * g, qd + off, kd + off, kIdescS, ks > 0 ? 1u : 0u);
         }
         if (g == tiles - 1) mma_commit(bar(B_KEMPTY + st));
         mma_commit(bar(B_SFULL + g));
-      };
-      for (int g = 0; g < tiles; ++g) issue_s(g, 0);
-      for (int n = 0; n < nt && ok; ++n) {
-        const int st = n & 1;
-        for (int g = 0; g < tiles && ok; ++g) {
-          wait(B_VFULL + st, n >> 1);
-          wait(B_PFULL + g, n);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t va = sbase + kOffV + st * kTile;
+      }
+      __syncwarp();
+    };
+    for (int g = 0; g < tiles; ++g) issue_s(g, 0);
+    for (int n = 0; n < nt && ok; ++n) {
+      const int st = n & 1;
+      for (int g = 0; g < tiles && ok; ++g) {
+        wait(B_VFULL + st, n >> 1);
+        wait(B_PFULL + g, n);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t vd = sw128_desc(sbase + kOffV + st * kTile, kHalf, 1024);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             // keys 16ks..16ks+15: P of a 32-column block sits in its first 16 columns
             mma_ts(tmem + kColO + 128u * g, tmem + 128u * g + 32u * (ks >> 1) + 8u * (ks & 1),
-                   sw128_desc(va + ks * 2048, kHalf, 1024), kIdescPV, (n > 0 || ks > 0) ? 1u : 0u);
+                   vd + ks * (2048 >> 4), kIdescPV, (n > 0 || ks > 0) ? 1u : 0u);
           if (g == tiles - 1) mma_commit(bar(B_VEMPTY + st));
           mma_commit(bar(B_PVDONE + g));
-          if (n + 1 < nt) issue_s(g, n + 1);
         }
+        __syncwarp();
+        if (n + 1 < nt) issue_s(g, n + 1);
       }
-      if (!ok) {
-        *abort_flag = 1;
-        // the copies of Q land before shared memory is released
-        for (int g = 0; g < tiles; ++g) mbar_wait(bar(B_QFULL + g), 0, nullptr);
-      }
-      mma_commit(bar(B_OFULL));
-      // TMEM is released only after every MMA issued here has completed.
-      mbar_wait(bar(B_OFULL), 0, nullptr);
     }
+    if (!ok) {
+      *abort_flag = 1;
+      // the copies of Q land before shared memory is released
+      for (int g = 0; g < tiles; ++g) mbar_wait(bar(B_QFULL + g), 0, nullptr);
+    }
+    if (elect_one()) mma_commit(bar(B_OFULL));
+    __syncwarp();
+    // TMEM is released only after every MMA issued here has completed.
+    mbar_wait(bar(B_OFULL), 0, nullptr);
   } else {
     // ------------------------------------------------------------ epilogue
-    const int e = warp - kDecWarps;
-    const int g = e >> 3, half = (e >> 2) & 1, q4 = warp & 3;
+    const int g = (warp - kEpi0) >> 2, q4 = warp & 3;
     const int r = 128 * g + 32 * q4 + lane;
     const bool row_ok = r < rows;
     const bool live = 128 * g + 32 * q4 < rows;    // the warp has candidates
     // rows past the last candidate repeat it, so that a warp's plans are of one kind
     const int cand = cand0 + min(r, rows - 1);
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16);
-    const uint32_t saddr = lane_addr + 128u * g + 64u * half;
+    const uint32_t saddr = lane_addr + 128u * g;
     const long long my_ts =
         TIME ? __ldg(a.cand_ts + checked(a.status, cand, a.C, BS_CAND4_ROW)) : 0ll;
-    const uint32_t* plan = TIME ? a.plan + static_cast<size_t>(key0 / 32 + 2 * half) * a.C + cand : nullptr;
-    auto plan_of = [&](int n, int cc) {
-      return (TIME && 128 * n + 64 * half + 32 * cc < keys)
-                 ? __ldg(plan + static_cast<size_t>(4 * n + cc) * a.C) : 0u;
+    // this candidate's time plans against tile n's four blocks, loaded a tile ahead
+    uint32_t pw[4] = {0u, 0u, 0u, 0u};
+    auto load_plans = [&](int n) {
+      const uint32_t* p = a.plan + static_cast<size_t>(key0 / 32 + 4 * n) * a.C + cand;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (128 * n + 32 * i < keys) pw[i] = __ldg(p + static_cast<size_t>(i) * a.C);
     };
-    uint32_t pw[2] = {0u, 0u};
-    if (live) {
-      pw[0] = plan_of(0, 0);
-      pw[1] = plan_of(0, 1);
-    }
+    if (TIME && live) load_plans(0);
     bool ok = true;
     for (int n = 0; n < nt && g < tiles; ++n) {
       const int slot = n & (kRing - 1);
@@ -408,36 +415,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (live) {
-        uint32_t nw[2] = {0u, 0u};
-        if (n + 1 < nt) {
-          nw[0] = plan_of(n + 1, 0);
-          nw[1] = plan_of(n + 1, 1);
-        }
 #pragma unroll 1
-        for (int cc = 0; cc < 2; ++cc) {
-          uint32_t sv[32];
-          tmem_ld32_nowait(saddr + 32u * cc, sv);
-          const int col = 64 * half + 32 * cc;           // first column of the tile
-          const int valid = keys - (128 * n + col);      // keys of this block
-          const float* pos = reinterpret_cast<const float*>(smem + kOffPos) + slot * 128 + col;
-          const uint32_t* ts32 = reinterpret_cast<const uint32_t*>(smem + kOffTs) + slot * 128 + col;
-          TimePlan tp{};
-          float tv[4] = {0.f, 0.f, 0.f, 0.f};
-          int tb = TB_NONE;
-          if (TIME && valid > 0) {
-            tb = plan_unword(tp, cc ? pw[1] : pw[0]);
-            if (tb >= TB_CONST && tb <= TB_MULTI) {
-              const int last = tb == TB_CONST ? 0 : tb == TB_SPLIT ? 1 : 3;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) tv[i] = tab.rabt()[max(tp.k_a - min(i, last), 0)];
-            }
-          }
-          tmem_wait_ld_dep(sv);
+        for (int cc = 0; cc < 4; ++cc) {
+          const int col = 32 * cc;                       // first column of the block
+          const int valid = keys - (128 * n + col);      // its keys
           uint32_t packed[16];
           if (valid <= 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) packed[i] = 0u;
           } else {
+            uint32_t sv[32];
+            tmem_ld32_nowait(saddr + col, sv);
+            const float* pos = reinterpret_cast<const float*>(smem + kOffPos) + slot * 128 + col;
+            const uint32_t* ts32 = reinterpret_cast<const uint32_t*>(smem + kOffTs) + slot * 128 + col;
+            TimePlan tp{};
+            float tv[4] = {0.f, 0.f, 0.f, 0.f};
+            int tb = TB_NONE;
+            if (TIME) {
+              tb = plan_unword(tp, pw[0]);
+              // blocks come in order: the next one's word moves up
+              pw[0] = pw[1];
+              pw[1] = pw[2];
+              pw[2] = pw[3];
+              tv[0] = tab.rabt()[tp.k_a];
+              tv[1] = tab.rabt()[max(tp.k_a - 1, 0)];
+            }
+            tmem_wait_ld_dep(sv);
             const uint32_t my32 = static_cast<uint32_t>(my_ts);
             if (!TIME || tb == TB_NONE) {
               p_block<POS, TB_NONE>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
@@ -446,6 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if (tb == TB_SPLIT) {
               p_block<POS, TB_SPLIT>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
             } else if (tb == TB_MULTI) {
+              tv[2] = tab.rabt()[max(tp.k_a - 2, 0)];
+              tv[3] = tab.rabt()[max(tp.k_a - 3, 0)];
               p_block<POS, TB_MULTI>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
             } else if (tb == TB_GEN32) {
               p_block<POS, TB_GEN32>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
@@ -474,15 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 packed[i] &= (2 * i < valid ? 0x0000FFFFu : 0u) | (2 * i + 1 < valid ? 0xFFFF0000u : 0u);
             }
           }
-          tmem_st16(saddr + 32u * cc, packed);   // over this warp's own S columns, already read
+          tmem_st16(saddr + col, packed);   // over this row's own S columns, already read
         }
-        pw[0] = nw[0];
-        pw[1] = nw[1];
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_PFULL + g));
+      if (TIME && live && n + 1 < nt) load_plans(n + 1);
     }
     if (ok) ok = flagged(mbar_wait(bar(B_OFULL), 0, abort_flag), a.status);
     ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
@@ -490,11 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && live) {
       tc_fence_after();
       const size_t D = static_cast<size_t>(a.H) * 128;
-      float* dst = a.part + (static_cast<size_t>(split) * a.C + cand) * D + h * 128 + 64 * half;
+      float* dst = a.part + (static_cast<size_t>(split) * a.C + cand) * D + h * 128;
 #pragma unroll 1
-      for (int cc = 0; cc < 2; ++cc) {
+      for (int cc = 0; cc < 4; ++cc) {
         uint32_t ov[32];
-        tmem_ld32_nowait(lane_addr + kColO + 128u * g + 64u * half + 32u * cc, ov);
+        tmem_ld32_nowait(lane_addr + kColO + 128u * g + 32u * cc, ov);
         tmem_wait_ld_dep(ov);
         if (row_ok) {
 #pragma unroll
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kDecWarps + kEpiWarps) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

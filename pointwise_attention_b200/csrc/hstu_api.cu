@@ -727,7 +727,7 @@ size_t hstu_cand_kv4_workspace_size(int32_t batch, int32_t num_heads, int32_t ma
     return 0;
   // [status][sums][time plans]
   return kStatusBytes +
-         align_up(cand4_part_rows(num_heads, max_seq_len, total_cands, max_cands) *
+         align_up(cand4_part_rows(batch, num_heads, max_seq_len, total_cands, max_cands) *
                   static_cast<size_t>(num_heads) * 512) +
          align_up(cand4_plan_bytes(max_seq_len, total_cands, max_cands));
 }
@@ -760,10 +760,13 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
   }
   if (p->dtype != HSTU_BF16 || p->d_qk != 128 || p->d_v != 128 || p->num_heads > 16)
     return HSTU_ERR_UNSUPPORTED;
-  const Cand4Cut cut = cand4_cut(p->batch, p->num_heads, p->max_seq_len, max_cands);
+  const Cand4Cut cut =
+      cand4_cut(p->batch, p->num_heads, p->max_seq_len, max_cands, p->total_tokens);
   // one grid dimension holds every (user, candidates, keys, heads) CTA, and
-  // every (user, candidate)
+  // every (user, candidate); the pieces of the histories are numbered in 32 bits
   if (static_cast<double>(p->batch) * cut.cgroups * cut.splits * cut.hgroups > 2147483647.0 ||
+      static_cast<double>(p->batch) * p->max_seq_len > 1e12 ||
+      (static_cast<double>(cut.ctas) + p->batch) * cut.parts * cut.hgroups > 2147483647.0 ||
       static_cast<double>(p->batch) * max_cands > 2147483647.0)
     return HSTU_ERR_UNSUPPORTED;
   // the plan pass: 8 blocks of 32 keys per CTA along a grid's y
@@ -815,7 +818,7 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
     if (p->rab_time) {
       uint32_t* plan = reinterpret_cast<uint32_t*>(
           static_cast<uint8_t*>(workspace) + kStatusBytes +
-          align_up(cand4_part_rows(p->num_heads, p->max_seq_len, total_cands, max_cands) *
+          align_up(cand4_part_rows(p->batch, p->num_heads, p->max_seq_len, total_cands, max_cands) *
                    static_cast<size_t>(p->num_heads) * 512));
       a.plan = plan;
       CandArgs pa;

@@ -245,14 +245,15 @@ struct Cand4Cut {
   int parts;     // few: warps that share a head's keys (many: 1)
   int hgroups;   // CTAs along the heads
   int nt;        // few: groups of 8 candidates of a CTA
-  int cgroups;   // CTAs along a user's candidates
-  int chunk, splits;   // history keys per CTA, CTAs along the longest history
+  int ctas;      // few: shares of the tokens
+  int cgroups;   // many: CTAs along a user's candidates
+  int chunk, splits;   // many: history keys per CTA, CTAs along the longest history
 };
-Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands);
-// Rows (of H*128 fp32) that hold the sums of every cut with H heads, histories
-// of at most max_seq_len and at most C candidates, max_cands a user, and the
+Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands, int total_tokens);
+// Rows (of H*128 fp32) that hold the sums of every cut with H heads, at most B
+// histories of max_seq_len and at most C candidates, max_cands a user, and the
 // bytes of the many-candidate kernel's time plans: both grow with each of them.
-size_t cand4_part_rows(int H, int max_seq_len, int C, int max_cands);
+size_t cand4_part_rows(int B, int H, int max_seq_len, int C, int max_cands);
 size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands);
 
 // The synchronous argument checks of hstu_attn_bwd (all but the workspace's).

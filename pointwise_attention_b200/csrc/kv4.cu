@@ -31,6 +31,7 @@ namespace hstu {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWords = 4;   // words of a thread, kThreads apart: that many loads in flight
 
 struct Kv4Args {
   const void* src[2];    // pack: k, v bf16 [T, H, 128]; unpack: codes
@@ -62,48 +63,68 @@ __device__ __forceinline__ bool cache_word(const Kv4Args& a, int64_t i, int64_t*
 // Four neighbouring lanes share a group of 32.
 __global__ void __launch_bounds__(kThreads) hstu_kv4_pack_rows(const Kv4Args a) {
   const int which = static_cast<int>(blockIdx.y);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const bool live = i < a.units;   // units is a multiple of 16: whole groups of lanes
-  uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-  if (live) raw = __ldg(static_cast<const uint4*>(a.src[which]) + i);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  // |x| as bit patterns: ordered like the values, NaN above infinity
-  uint32_t m = 0;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kWords) + threadIdx.x;
+  uint4 raw[kWords];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    m = max(m, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const float s = kv4_scale(m);
-  const float inv = 1.0f / s;
-  uint32_t code = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t lo = kv4_code(__uint_as_float(w[e] << 16) * inv);
-    const uint32_t hi = kv4_code(__uint_as_float(w[e] & 0xFFFF0000u) * inv);
-    code |= (lo << (4 * e)) | (hi << (16 + 4 * e));
+  for (int j = 0; j < kWords; ++j) {
+    const int64_t i = i0 + j * kThreads;   // units is a multiple of 16: whole groups of lanes
+    raw[j] = i < a.units ? __ldg(static_cast<const uint4*>(a.src[which]) + i)
+                         : make_uint4(0u, 0u, 0u, 0u);
   }
-  int64_t at;
-  if (!live || !cache_word(a, i, &at)) return;
-  static_cast<uint32_t*>(a.dst[which])[at] = code;
-  if ((at & 3) == 0)
-    static_cast<__nv_bfloat16*>(a.scales[which])[at >> 2] = __float2bfloat16_rn(s);   // exact
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    const int64_t i = i0 + j * kThreads;
+    const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+    // |x| as bit patterns: ordered like the values, NaN above infinity
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      m = max(m, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float s = kv4_scale(m);
+    const float inv = 1.0f / s;
+    uint32_t code = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = kv4_code(__uint_as_float(w[e] << 16) * inv);
+      const uint32_t hi = kv4_code(__uint_as_float(w[e] & 0xFFFF0000u) * inv);
+      code |= (lo << (4 * e)) | (hi << (16 + 4 * e));
+    }
+    int64_t at;
+    if (i >= a.units || !cache_word(a, i, &at)) continue;
+    static_cast<uint32_t*>(a.dst[which])[at] = code;
+    if ((at & 3) == 0)
+      static_cast<__nv_bfloat16*>(a.scales[which])[at >> 2] = __float2bfloat16_rn(s);   // exact
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) hstu_kv4_unpack_rows(const Kv4Args a) {
   const int which = static_cast<int>(blockIdx.y);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  int64_t at;
-  if (i >= a.units || !cache_word(a, i, &at)) return;
-  const uint32_t code = __ldg(static_cast<const uint32_t*>(a.src[which]) + at);
-  const uint32_t s = __ldg(static_cast<const uint16_t*>(a.scales[which]) + (at >> 2));
-  const uint32_t s2 = s | (s << 16);
-  uint4 o;
-  o.x = kv4_pair<0>(code, s2);
-  o.y = kv4_pair<1>(code, s2);
-  o.z = kv4_pair<2>(code, s2);
-  o.w = kv4_pair<3>(code, s2);
-  static_cast<uint4*>(a.dst[which])[i] = o;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kWords) + threadIdx.x;
+  uint32_t code[kWords], scale[kWords];
+  bool live[kWords];
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    const int64_t i = i0 + j * kThreads;
+    int64_t at;
+    live[j] = i < a.units && cache_word(a, i, &at);
+    if (live[j]) {
+      code[j] = __ldg(static_cast<const uint32_t*>(a.src[which]) + at);
+      scale[j] = __ldg(static_cast<const uint16_t*>(a.scales[which]) + (at >> 2));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    if (!live[j]) continue;
+    const uint32_t s2 = scale[j] | (scale[j] << 16);
+    uint4 o;
+    o.x = kv4_pair<0>(code[j], s2);
+    o.y = kv4_pair<1>(code[j], s2);
+    o.z = kv4_pair<2>(code[j], s2);
+    o.w = kv4_pair<3>(code[j], s2);
+    static_cast<uint4*>(a.dst[which])[i0 + j * kThreads] = o;
+  }
 }
 
 struct Kv4Range {
@@ -121,7 +142,7 @@ hstu_status_t run(bool pack, int32_t T, int32_t H, int32_t cache_rows, const int
       if (!p || reinterpret_cast<uintptr_t>(p) % 16 != 0) return HSTU_ERR_INVALID_ARG;
   }
   if (reinterpret_cast<uintptr_t>(rows) % 4 != 0) return HSTU_ERR_INVALID_ARG;
-  // one thread per word, 256 a block, blocks in grid x
+  // blocks of kThreads * kWords words in grid x
   const int64_t units = 16ll * T * H;
   if (H > 65536 || units > 0x7FFFFFFFll * kThreads) return HSTU_ERR_UNSUPPORTED;
   // only the cache rows given by index can be found wrong on the device
@@ -141,7 +162,8 @@ hstu_status_t run(bool pack, int32_t T, int32_t H, int32_t cache_rows, const int
   a.units = units;
   a.H = H;
   a.R = cache_rows;
-  const dim3 grid(static_cast<unsigned>((units + kThreads - 1) / kThreads), 2);
+  constexpr int64_t kBlock = kThreads * kWords;
+  const dim3 grid(static_cast<unsigned>((units + kBlock - 1) / kBlock), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pack)
     hstu_kv4_pack_rows<<<grid, kThreads, 0, s>>>(a);

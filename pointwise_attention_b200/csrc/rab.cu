@@ -82,16 +82,15 @@ __global__ void __launch_bounds__(kFwdThreads) hstu_rab_fwd(const __grid_constan
 }
 
 constexpr int kBwdWarps = 16;
-constexpr int kBatch = 8;   // loads of a warp in flight
+constexpr int kPiece = 1024;   // distances of a piece: 32 loads a lane
 
-// One cluster per head; its CTAs split the distances, their warps split a
-// CTA's part into neighbouring runs.  A warp walks its run 32 distances at a
-// time: while a whole step lies in one bucket the lanes add to a register,
-// and at a border the register and the step's segments (a segmented scan over
-// the lanes) go to the warp's own sums in shared memory.  Warps, then CTAs,
-// are added in order, so the result does not depend on timing.
+// One cluster per head.  A bucket's distances are cut into pieces of kPiece, so
+// that no piece crosses a border; the cluster's warps take pieces in turn and
+// add each one's sum to their own sum of its bucket, in order.  Warps, then
+// CTAs, are added in order too, so the result does not depend on timing.
 __global__ void __launch_bounds__(32 * kBwdWarps) hstu_rab_bwd(const __grid_constant__ RabArgs a) {
-  __shared__ int thr[kMaxBuckets];
+  __shared__ int start[kMaxBuckets + 1];   // first distance of each bucket
+  __shared__ int piece0[kMaxBuckets + 1];  // first piece of each bucket
   __shared__ float part[kBwdWarps][kMaxBuckets];
   __shared__ float total[kMaxBuckets];
   cg::cluster_group cluster = cg::this_cluster();
@@ -99,63 +98,60 @@ __global__ void __launch_bounds__(32 * kBwdWarps) hstu_rab_bwd(const __grid_cons
   const int rank = static_cast<int>(cluster.block_rank());
   const int h = static_cast<int>(blockIdx.y);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  for (int i = static_cast<int>(threadIdx.x); i < kMaxBuckets; i += 32 * kBwdWarps) thr[i] = a.thr[i];
+  for (int i = static_cast<int>(threadIdx.x); i <= kMaxBuckets; i += 32 * kBwdWarps)
+    start[i] = i == 0 ? 0 : i >= a.nb ? a.L : min(a.thr[i - 1], a.L);
   for (int i = static_cast<int>(threadIdx.x); i < kBwdWarps * kMaxBuckets; i += 32 * kBwdWarps)
     part[i / kMaxBuckets][i % kMaxBuckets] = 0.f;
   __syncthreads();
+  if (warp == 0) {
+    // running count of pieces: four buckets per lane, a scan over the lanes
+    int n[4], own = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      n[e] = (start[4 * lane + e + 1] - start[4 * lane + e] + kPiece - 1) / kPiece;
+      own += n[e];
+    }
+    int up = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += y;
+    }
+    int at = up - own;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      piece0[4 * lane + e] = at;
+      at += n[e];
+    }
+    if (lane == 31) piece0[kMaxBuckets] = at;
+  }
+  __syncthreads();
 
   const float* g = a.in + static_cast<size_t>(h) * (2 * static_cast<size_t>(a.L) - 1) + (a.L - 1);
-  const int64_t workers = static_cast<int64_t>(ranks) * kBwdWarps;
-  const int64_t run = ((a.L + workers - 1) / workers + 31) / 32 * 32;   // per warp, whole steps
-  const int64_t begin = (static_cast<int64_t>(rank) * kBwdWarps + warp) * run;
-  const int end = static_cast<int>(begin + run < a.L ? begin + run : a.L);
-  float* mine = part[warp];
-  float acc = 0.f;
-  int cur = begin < end ? find_bucket(thr, static_cast<int>(begin)) : 0;   // bucket of the next step's first distance
-  for (int64_t at = begin; at < end; at += 32 * kBatch) {
-    float v[kBatch];
+  const int pieces = piece0[kMaxBuckets];
+  for (int p = rank + ranks * warp; p < pieces; p += ranks * kBwdWarps) {
+    int k = 0;   // the last bucket whose first piece is at or before p
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      const int64_t d = at + 32 * s + lane;
-      v[s] = d < end ? __ldg(g + d) : 0.f;
+    for (int step = kMaxBuckets / 2; step > 0; step >>= 1)
+      if (piece0[k + step] <= p) k += step;
+    const int lo = start[k] + (p - piece0[k]) * kPiece, n = min(kPiece, start[k + 1] - lo);
+    float sum = 0.f;
+    if (n <= 256) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (32 * i + lane < n) sum += __ldg(g + lo + 32 * i + lane);
+    } else {
+      float v[kPiece / 32];
+#pragma unroll
+      for (int i = 0; i < kPiece / 32; ++i)
+        v[i] = 32 * i + lane < n ? __ldg(g + lo + 32 * i + lane) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kPiece / 32; ++i) sum += v[i];
     }
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      const int64_t d64 = at + 32 * s;
-      if (d64 >= end) break;
-      const int d = static_cast<int>(d64);
-      // the distances of this step that the run has (the others add zeros)
-      const int last = d + 31 < end - 1 ? d + 31 : end - 1;
-      if (thr[cur] > last || cur == kMaxBuckets - 1) {
-        acc += v[s];
-        continue;
-      }
-      // a border: the register's sum first, then this step's segments
-      float sum = acc;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) mine[cur] += sum;
-      acc = 0.f;
-      __syncwarp();
-      const int b = find_bucket(thr, d + lane < last ? d + lane : last);
-      float x = v[s];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, x, o);
-        const int yb = __shfl_up_sync(0xffffffffu, b, o);
-        if (lane >= o && yb == b) x += y;
-      }
-      const int nxt = __shfl_down_sync(0xffffffffu, b, 1);
-      if (lane == 31 || nxt != b) mine[b] += x;   // one lane per bucket
-      __syncwarp();
-      cur = __shfl_sync(0xffffffffu, b, 31);
-      if (last + 1 < end) cur = find_bucket(thr, last + 1);
-    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[warp][k] += sum;
   }
-  float sum = acc;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0 && begin < end) mine[cur] += sum;
   __syncthreads();
   for (int k = static_cast<int>(threadIdx.x); k < a.nb; k += 32 * kBwdWarps) {
     float s = 0.f;
@@ -289,7 +285,8 @@ HSTU_API hstu_status_t hstu_rab_bucket_bwd(int32_t H, int32_t L, int32_t num_buc
   RabArgs a;
   const hstu_status_t st = fill(&a, H, L, num_buckets, thresholds, d_rab_pos, d_table);
   if (st != HSTU_OK || H == 0) return st;
-  // one CTA takes 4096 distances (8 loads a lane) before a second one joins it
+  // about one piece a warp: a CTA's 16 warps take their buckets' short pieces
+  // and 4096 distances before a second CTA joins it
   unsigned ranks = 1;
   while (ranks < 8 && static_cast<int64_t>(ranks) * 4096 < L) ranks *= 2;
   cudaLaunchConfig_t cfg = {};

@@ -24,6 +24,7 @@
 
 #include "hstu.h"
 #include "internal.h"
+#include "tile_math.cuh"
 
 namespace hstu {
 namespace {
@@ -150,33 +151,69 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
 template <int TPR>
 constexpr int block_threads() { return TPR == 32 ? 256 : TPR; }
 
+// The arithmetic runs on pairs of neighbouring owned elements (fp32 pairs: one
+// instruction for two), which halves the issue slots that bound these kernels
+// beside HBM.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ uint64_t get_pair(const Pack<T, VEC> (&p)[NV], int i) {
+  const int a = 2 * i, b = 2 * i + 1;
+  return pack_f32x2(Elem<T>::get(p[a / VEC].v[a % VEC]), Elem<T>::get(p[b / VEC].v[b % VEC]));
+}
+
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void put_pair(Pack<T, VEC> (&p)[NV], int i, uint64_t v) {
+  const int a = 2 * i, b = 2 * i + 1;
+  const float2 f = unpack_f32x2(v);
+  if constexpr (sizeof(T) == 2 && VEC % 2 == 0) {
+    *reinterpret_cast<uint32_t*>(&p[a / VEC].v[a % VEC]) = pack_bf16x2(f.x, f.y);
+  } else {
+    p[a / VEC].v[a % VEC] = Elem<T>::put(f.x);
+    p[b / VEC].v[b % VEC] = Elem<T>::put(f.y);
+  }
+}
+
+// Larger magnitude; a NaN on either side gives a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+  return d;
+}
+
 // NORM: the norm; otherwise the rows as they are (quantisation alone).
 template <typename T, int VEC, int TPR, int NV, bool NORM>
-__global__ void __launch_bounds__(block_threads<TPR>()) hstu_rows_fwd(const RowsArgs a) {
+__global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / block_threads<TPR>() : 1)
+    hstu_rows_fwd(const RowsArgs a) {
   constexpr int kRows = block_threads<TPR>() / TPR;   // rows of a block at a time
-  constexpr int N = NV * VEC;
+  constexpr int N = NV * VEC, P = N / 2;
   __shared__ float red[TPR > 32 ? TPR / 32 : 1];
   const int lane = TPR == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int sub = TPR == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.res);
-  float w[N];
-  if (NORM) load_weight<VEC, TPR, NV>(a.weight, lane, a.E, w);
-  // the loop is uniform over the threads of a row, and over the block where
-  // the block is the row
-  for (int t = static_cast<int>(blockIdx.x) * kRows + sub; t < a.T;
-       t += static_cast<int>(gridDim.x) * kRows) {
+  uint64_t w[P];
+  if (NORM) {
+    float f[N];
+    load_weight<VEC, TPR, NV>(a.weight, lane, a.E, f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) w[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
+  }
+  // The loop is uniform over the threads of a row, and over the block where
+  // the block is the row.  The next row's loads are issued before this row's
+  // sums are waited for.
+  const int stride = static_cast<int>(gridDim.x) * kRows;
+  int t = static_cast<int>(blockIdx.x) * kRows + sub;
+  Pack<T, VEC> p[NV], q[NV];
+  auto load = [&](int row) {
+    load_row<T, VEC, TPR, NV>(x + static_cast<size_t>(row) * a.E, lane, a.E, p);
+    if (NORM && res) load_row<T, VEC, TPR, NV>(res + static_cast<size_t>(row) * a.E, lane, a.E, q);
+  };
+  if (t < a.T) load(t);
+  for (; t < a.T; t += stride) {
     const size_t at = static_cast<size_t>(t) * a.E;
-    Pack<T, VEC> p[NV];
-    load_row<T, VEC, TPR, NV>(x + at, lane, a.E, p);
     if (NORM && res) {
-      Pack<T, VEC> q[NV];
-      load_row<T, VEC, TPR, NV>(res + at, lane, a.E, q);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          p[i].v[e] = Elem<T>::put(Elem<T>::get(p[i].v[e]) + Elem<T>::get(q[i].v[e]));
+      for (int i = 0; i < P; ++i)
+        put_pair<T, VEC, NV>(p, i, fadd2(get_pair<T, VEC, NV>(p, i), get_pair<T, VEC, NV>(q, i)));
       if (a.h) {
         T* h = static_cast<T*>(a.h) + at;
 #pragma unroll
@@ -186,98 +223,147 @@ __global__ void __launch_bounds__(block_threads<TPR>()) hstu_rows_fwd(const Rows
         }
       }
     }
-    float v[N];
+    uint64_t v[P];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = Elem<T>::get(p[i / VEC].v[i % VEC]);
+    for (int i = 0; i < P; ++i) v[i] = get_pair<T, VEC, NV>(p, i);
+    if (t < a.T - stride) load(t + stride);
     if (NORM) {
-      float ss = 0.f;
+      uint64_t ss2 = 0ull;
 #pragma unroll
-      for (int i = 0; i < N; ++i) ss = fmaf(v[i], v[i], ss);
-      ss = row_sum<TPR>(ss, red);
+      for (int i = 0; i < P; ++i) ss2 = ffma2(v[i], v[i], ss2);
+      const float2 s2 = unpack_f32x2(ss2);
+      const float ss = row_sum<TPR>(s2.x + s2.y, red);
       const float r = 1.0f / sqrtf(ss / static_cast<float>(a.E) + a.eps);
       if (a.rstd && lane == 0) a.rstd[t] = r;
+      const uint64_t r2 = pack_f32x2(r, r);
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] * r * w[i];
+      for (int i = 0; i < P; ++i) v[i] = fmul2(fmul2(v[i], r2), w[i]);
       if (a.y) {
         T* y = static_cast<T*>(a.y) + at;
+        Pack<T, VEC> o[NV];
+#pragma unroll
+        for (int i = 0; i < P; ++i) put_pair<T, VEC, NV>(o, i, v[i]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = (i * TPR + lane) * VEC;
-          Pack<T, VEC> o;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) o.v[e] = Elem<T>::put(v[i * VEC + e]);
-          if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(y + c) = o;
+          if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(y + c) = o[i];
         }
       }
     }
     if (!NORM || a.q8) {
-      // The maximum goes over bit patterns: those of |v| are ordered like the
-      // values, with NaN above infinity, so that a NaN reaches the scale.
-      uint32_t m = 0;
+      // The threads' maxima meet as bit patterns: those of |v| are ordered
+      // like the values, with NaN above infinity, so that a NaN reaches the
+      // scale.
+      float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      m = row_umax<TPR>(m, reinterpret_cast<uint32_t*>(red));
-      const float top = __uint_as_float(m);
+      for (int i = 0; i < P; ++i) {
+        const float2 f = unpack_f32x2(v[i]);
+        m = max_nan(max_nan(m, f.x), f.y);
+      }
+      const float top =
+          __uint_as_float(row_umax<TPR>(__float_as_uint(m), reinterpret_cast<uint32_t*>(red)));
       const float s = (top < kAmaxFloor ? kAmaxFloor : top) / kE4M3Max;
       const float inv = 1.0f / s;
       if (lane == 0) a.scale[t] = s;
       uint8_t* q8 = a.q8 + at;
+      const uint64_t inv2 = pack_f32x2(inv, inv);
+      Pack<uint8_t, VEC> o[NV];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const __nv_fp8x2_storage_t c =
+            __nv_cvt_float2_to_fp8x2(unpack_f32x2(fmul2(v[i], inv2)), __NV_SATFINITE, __NV_E4M3);
+        if constexpr (VEC % 2 == 0) {
+          *reinterpret_cast<__nv_fp8x2_storage_t*>(&o[2 * i / VEC].v[2 * i % VEC]) = c;
+        } else {
+          o[2 * i].v[0] = static_cast<uint8_t>(c & 0xFFu);
+          o[2 * i + 1].v[0] = static_cast<uint8_t>(c >> 8);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * VEC;
-        Pack<uint8_t, VEC> o;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          o.v[e] = __nv_cvt_float_to_fp8(v[i * VEC + e] * inv, __NV_SATFINITE, __NV_E4M3);
-        if (c < a.E) *reinterpret_cast<Pack<uint8_t, VEC>*>(q8 + c) = o;
+        if (c < a.E) *reinterpret_cast<Pack<uint8_t, VEC>*>(q8 + c) = o[i];
       }
     }
   }
 }
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(block_threads<TPR>()) hstu_rows_bwd(const RowsBwdArgs a) {
+__global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 512 / block_threads<TPR>() : 1)
+    hstu_rows_bwd(const RowsBwdArgs a) {
   constexpr int kRows = block_threads<TPR>() / TPR;
-  constexpr int N = NV * VEC;
+  constexpr int N = NV * VEC, P = N / 2;
   __shared__ float red[TPR > 32 ? TPR / 32 : 1];
   __shared__ float sdw[TPR == 32 ? kRows : 1][TPR == 32 ? 32 * N : 1];
   const int lane = TPR == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int sub = TPR == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
-  float w[N], dw[N];
-  load_weight<VEC, TPR, NV>(a.weight, lane, a.E, w);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  uint64_t w[P], dw2[P];
+  {
+    float f[N];
+    load_weight<VEC, TPR, NV>(a.weight, lane, a.E, f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) dw[i] = 0.f;
-  for (int t = static_cast<int>(blockIdx.x) * kRows + sub; t < a.T;
-       t += static_cast<int>(gridDim.x) * kRows) {
-    const size_t at = static_cast<size_t>(t) * a.E;
-    Pack<T, VEC> pd[NV], ph[NV], pr[NV];
+    for (int i = 0; i < P; ++i) {
+      w[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
+      dw2[i] = 0ull;
+    }
+  }
+  const int stride = static_cast<int>(gridDim.x) * kRows;
+  int t = static_cast<int>(blockIdx.x) * kRows + sub;
+  Pack<T, VEC> pd[NV], ph[NV], pr[NV];
+  float rn = 0.f;
+  auto load = [&](int row) {
+    const size_t at = static_cast<size_t>(row) * a.E;
     load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.dy) + at, lane, a.E, pd);
     load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.h) + at, lane, a.E, ph);
+    rn = __ldg(a.rstd + row);
+  };
+  // the next row's dy and h are loaded before this row's sum is waited for,
+  // and this row's d_residual while it is added up
+  // (wider rows have enough loads in flight, and no registers to spare)
+  constexpr bool kAhead = N <= 16;
+  if (kAhead && t < a.T) load(t);
+  for (; t < a.T; t += stride) {
+    const size_t at = static_cast<size_t>(t) * a.E;
+    if (!kAhead) load(t);
     if (a.dres) load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.dres) + at, lane, a.E, pr);
-    const float r = __ldg(a.rstd + t);
-    float dot = 0.f;
+    const float r = rn;
+    const uint64_t r2 = pack_f32x2(r, r);
+    // g = w dy and z = h r: dx = r g - z (r mean(g z)), dw += dy z
+    uint64_t g[P], z[P], dot2 = 0ull;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = Elem<T>::get(pd[i / VEC].v[i % VEC]), h = Elem<T>::get(ph[i / VEC].v[i % VEC]);
-      dot = fmaf(d * w[i], h, dot);
-      dw[i] = fmaf(d * h, r, dw[i]);
+    for (int i = 0; i < P; ++i) {
+      const uint64_t d = get_pair<T, VEC, NV>(pd, i);
+      z[i] = fmul2(get_pair<T, VEC, NV>(ph, i), r2);
+      g[i] = fmul2(d, w[i]);
+      dot2 = ffma2(g[i], z[i], dot2);
+      dw2[i] = ffma2(d, z[i], dw2[i]);
     }
-    dot = row_sum<TPR>(dot, red);
-    const float k = r * r * (dot / static_cast<float>(a.E));
+    if (kAhead && t < a.T - stride) load(t + stride);
+    const float2 d2 = unpack_f32x2(dot2);
+    const float dot = row_sum<TPR>(d2.x + d2.y, red);
+    const float k = -r * (dot / static_cast<float>(a.E));
+    const uint64_t k2 = pack_f32x2(k, k);
     T* dx = static_cast<T*>(a.dx) + at;
+    Pack<T, VEC> o[NV];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      uint64_t x = ffma2(z[i], k2, fmul2(g[i], r2));
+      if (a.dres) x = fadd2(x, get_pair<T, VEC, NV>(pr, i));
+      put_pair<T, VEC, NV>(o, i, x);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * VEC;
-      Pack<T, VEC> o;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = Elem<T>::get(pd[i].v[e]), h = Elem<T>::get(ph[i].v[e]);
-        float g = r * fmaf(-h, k, d * w[i * VEC + e]);
-        if (a.dres) g += Elem<T>::get(pr[i].v[e]);
-        o.v[e] = Elem<T>::put(g);
-      }
-      if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(dx + c) = o;
+      if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(dx + c) = o[i];
     }
+  }
+  float dw[N];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const float2 f = unpack_f32x2(dw2[i]);
+    dw[2 * i] = f.x;
+    dw[2 * i + 1] = f.y;
   }
   if (!a.partial) return;
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * a.E;
@@ -308,9 +394,19 @@ __global__ void __launch_bounds__(1024) hstu_rows_dw(const float* partial, int b
   __shared__ float red[32][33];
   const int cx = static_cast<int>(threadIdx.x & 31), gy = static_cast<int>(threadIdx.x >> 5);
   const int c = static_cast<int>(blockIdx.x) * 32 + cx;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the rows' kernel runs
   float s = 0.f;
-  if (c < E)
-    for (int g = gy; g < blocks; g += 32) s += partial[static_cast<size_t>(g) * E + c];
+  if (c < E) {
+    // eight loads in flight, added in order
+    for (int g = gy; g < blocks; g += 256) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = g + 32 * i < blocks ? partial[static_cast<size_t>(g + 32 * i) * E + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+  }
   red[gy][cx] = s;
   __syncthreads();
   s = warp_sum(red[cx][gy]);   // column gy of the tile
@@ -369,7 +465,9 @@ cudaError_t launch_rows_fwd(const RowsArgs& a, cudaStream_t stream) {
   return pick_shape<T>(vec, a.E, [&](auto s) {
     using S = decltype(s);
     constexpr int kRows = block_threads<S::TPR>() / S::TPR;
-    const int blocks = static_cast<int>((static_cast<int64_t>(a.T) + kRows - 1) / kRows);
+    // eight blocks per SM at most: each row's loads then run ahead of it
+    const int64_t need = (static_cast<int64_t>(a.T) + kRows - 1) / kRows;
+    const int blocks = static_cast<int>(need < 8 * 148 ? need : 8 * 148);
     hstu_rows_fwd<T, S::VEC, S::TPR, S::NV, NORM>
         <<<blocks, block_threads<S::TPR>(), 0, stream>>>(a);
     return cudaGetLastError();
@@ -398,8 +496,16 @@ cudaError_t launch_rows_bwd(const RowsBwdArgs& a, float* dw, cudaStream_t stream
     return cudaGetLastError();
   });
   if (err != cudaSuccess || !dw) return err;
-  hstu_rows_dw<<<(a.E + 31) / 32, 1024, 0, stream>>>(a.partial, blocks, a.E, dw);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.E + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, hstu_rows_dw, static_cast<const float*>(a.partial), blocks, a.E, dw);
 }
 
 size_t elem_bytes(hstu_dtype_t d) { return d == HSTU_BF16 ? 2 : 4; }
