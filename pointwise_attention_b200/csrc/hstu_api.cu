@@ -574,7 +574,7 @@ hstu_status_t hstu_uvqk_fp8_fwd(int32_t T, int32_t E, int32_t H, int32_t d_qk, i
   a.vec32 = al32(u) && al32(v) && al32(q) && al32(k);
   const int N = static_cast<int>(2 * (Nu + Nq));
   CUtensorMap tx, tw;
-  if (!make_map_2d_u8(&tx, x8, T, E, 128) || !make_map_2d_u8(&tw, w8, N, E, uvqk_fp8_cols(T, N)))
+  if (!make_map_2d_u8(&tx, x8, T, E, 128) || !make_map_2d_u8(&tw, w8, N, E, uvqk_fp8_cols(T, E, N)))
     return HSTU_ERR_CUDA;
   const cudaError_t err = launch_uvqk_fp8_sm100(a, tx, tw, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;

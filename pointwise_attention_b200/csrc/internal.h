@@ -279,7 +279,7 @@ cudaError_t launch_cand4_finish(const Cand4Args& a, const Cand4Cut& cut, bool af
                                 cudaStream_t stream);
 cudaError_t launch_uvqk_sm100(const ProjArgs& a, const CUtensorMap& tx, const CUtensorMap& tw,
                               cudaStream_t stream);
-int uvqk_fp8_cols(int T, int N);   // columns of a tile of the 8-bit projection
+int uvqk_fp8_cols(int T, int E, int N);   // columns of a tile of the 8-bit projection
 cudaError_t launch_uvqk_fp8_sm100(const Proj8Args& a, const CUtensorMap& tx, const CUtensorMap& tw,
                                   cudaStream_t stream);
 cudaError_t launch_out_sm100(const ProjArgs& a, const CUtensorMap& ty, const CUtensorMap& tw,

@@ -217,10 +217,11 @@ def project(seed, T, E, H, dqk, dv, act, bias, what):
     if b is not None:
         p = p + b.double()
     # fp32 sums of E products, four roundings after them; SiLU's slope is at
-    # most 1.1 and its exponential and quotient are good to 2^-20
+    # most 1.1, and it is x/2 (1 + tanh(x/2)) with the hardware's tanh, whose
+    # documented relative error is 2^-11: |x|/2 2^-11
     tol = mag * (E + 4) * U + p.abs() * 4 * U
     if act:
-        p, tol = silu64(p), 1.1 * tol + silu64(p).abs() * 2.0 ** -20
+        p, tol = silu64(p), 1.1 * tol + p.abs() * 2.0 ** -12
     tol = tol + p.abs() * HALF[BF16] + 1e-30
     at = 0
     for n, w_ in (("u", dv), ("v", dv), ("q", dqk), ("k", dqk)):
