@@ -141,6 +141,21 @@ bool make_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
   return r == CUDA_SUCCESS;
 }
 
+// [rows, cols] bf16 row-major as a 2-D tensor (col, row); box = 32 x 32,
+// 64-byte swizzle (for stores: rows past `rows` are not written).
+bool make_map_2d_out(CUtensorMap* map, void* base, int64_t rows, int64_t cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  cuuint32_t box[2] = {32, 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // [rows, cols] bytes row-major as a 2-D tensor (col, row); box = 128 x box_rows,
 // 128-byte swizzle.  Rows past `rows` and columns past `cols` read as zeros.
 bool make_map_2d_u8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows) {
@@ -576,7 +591,11 @@ hstu_status_t hstu_uvqk_fp8_fwd(int32_t T, int32_t E, int32_t H, int32_t d_qk, i
   CUtensorMap tx, tw;
   if (!make_map_2d_u8(&tx, x8, T, E, 128) || !make_map_2d_u8(&tw, w8, N, E, uvqk_fp8_cols(T, E, N)))
     return HSTU_ERR_CUDA;
-  const cudaError_t err = launch_uvqk_fp8_sm100(a, tx, tw, static_cast<cudaStream_t>(stream));
+  Proj8Outs to;
+  void* const out[4] = {u, v, q, k};
+  for (int i = 0; i < 4; ++i)
+    if (!make_map_2d_out(&to.map[i], out[i], T, i < 2 ? Nu : Nq)) return HSTU_ERR_CUDA;
+  const cudaError_t err = launch_uvqk_fp8_sm100(a, tx, tw, to, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 

@@ -171,6 +171,12 @@ struct Proj8Args {
   int vec32;                // every output pointer is 32-byte aligned
 };
 
+// The outputs u, v, q, k as [T, columns] bf16, boxes of 32 columns x 32 rows
+// with the 64-byte swizzle.
+struct Proj8Outs {
+  CUtensorMap map[4];
+};
+
 // Arguments of the candidate-scoring kernel (scoring against cached histories).
 struct CandArgs {
   const int32_t* offsets;        // history [B+1]
@@ -281,7 +287,7 @@ cudaError_t launch_uvqk_sm100(const ProjArgs& a, const CUtensorMap& tx, const CU
                               cudaStream_t stream);
 int uvqk_fp8_cols(int T, int E, int N);   // columns of a tile of the 8-bit projection
 cudaError_t launch_uvqk_fp8_sm100(const Proj8Args& a, const CUtensorMap& tx, const CUtensorMap& tw,
-                                  cudaStream_t stream);
+                                  const Proj8Outs& to, cudaStream_t stream);
 cudaError_t launch_out_sm100(const ProjArgs& a, const CUtensorMap& ty, const CUtensorMap& tw,
                              cudaStream_t stream);
 cudaError_t launch_time_plans(const PlanArgs& a, cudaStream_t stream);

@@ -53,15 +53,22 @@ __device__ __forceinline__ uint64_t silu2(uint64_t h2) {
 
 // The output tensor and column that column n0 of the projection belongs to.
 struct Dest {
-  __nv_bfloat16* base;
-  int ld;
+  __nv_bfloat16* base;   // of column n0
+  int ld, which, col;    // which output tensor, and the column in it
 };
 __device__ __forceinline__ Dest dest_of(const Proj8Args& a, int n0) {
   const int Nu = a.Nu, Nq = a.Nq;
-  if (n0 < Nu) return {static_cast<__nv_bfloat16*>(a.out0) + n0, Nu};
-  if (n0 < 2 * Nu) return {static_cast<__nv_bfloat16*>(a.out1) + (n0 - Nu), Nu};
-  if (n0 < 2 * Nu + Nq) return {static_cast<__nv_bfloat16*>(a.out2) + (n0 - 2 * Nu), Nq};
-  return {static_cast<__nv_bfloat16*>(a.out3) + (n0 - 2 * Nu - Nq), Nq};
+  int which = 0, col = n0;
+  if (col >= 2 * Nu) {
+    col -= 2 * Nu;
+    which = 2 + (col >= Nq);
+    col -= which == 3 ? Nq : 0;
+  } else if (col >= Nu) {
+    col -= Nu;
+    which = 1;
+  }
+  void* const out[4] = {a.out0, a.out1, a.out2, a.out3};
+  return {static_cast<__nv_bfloat16*>(out[which]) + col, which < 2 ? Nu : Nq, which, col};
 }
 
 // 32 neighbouring outputs of a row from their accumulators: (acc sx) sw + b,
@@ -110,12 +117,14 @@ __device__ __forceinline__ void load_columns(const Proj8Args& a, int n0, float* 
 }
 
 // ------------------------------------------------------- W in shared memory
-constexpr int kStagesX = 5;
+constexpr int kStagesX = 3;
 constexpr int kMaxW = 131072;              // bytes of W8 kept: NT columns x (E up to 128s)
 
 template <int NT>
 struct Keep {
-  static constexpr int S = NT >= 64 ? 2 : 1;   // epilogue warps per TMEM lane quarter
+  // Epilogue warps per TMEM lane quarter: with two of them (eight warps) the
+  // epilogue's latencies bound 131072 x 512 x 2048 at 177 us.
+  static constexpr int S = NT >= 128 ? 4 : NT / 32;
   static constexpr int kThreads = 64 + 128 * S;
   static constexpr int kCols = NT / S;         // per epilogue thread
   static constexpr int kTmem = 2 * NT;         // two accumulators
@@ -123,7 +132,10 @@ struct Keep {
   static constexpr int B_XFULL = 0, B_XEMPTY = kStagesX, B_W = 2 * kStagesX, B_TFULL = B_W + 1,
                        B_TEMPTY = B_TFULL + 2, kNumBars = B_TEMPTY + 2;
   static constexpr int kOffX = 0;                           // stages of X
-  static constexpr int kOffCols = kStagesX * kABytes;       // float [2][NT]
+  // Outputs leave by TMA, 32 rows x 32 columns a warp at a time: stores of the
+  // threads themselves (a row each) kept the load/store unit 91% busy.
+  static constexpr int kOffOut = kStagesX * kABytes;        // 2 KB a warp
+  static constexpr int kOffCols = kOffOut + 4 * S * 2048;   // float [2][NT]
   static constexpr int kOffBar = kOffCols + 8 * NT;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kOffW = (kOffMisc + 16 + 1023) / 1024 * 1024;
@@ -135,7 +147,7 @@ static_assert(Keep<256>::kOffW + kMaxW + 1024 <= 227 * 1024, "shared memory per 
 template <int NT>
 __global__ void __launch_bounds__(Keep<NT>::kThreads, 1)
     uvqk_fp8_keep(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                  const __grid_constant__ Proj8Args a) {
+                  const __grid_constant__ Proj8Outs tm_out, const __grid_constant__ Proj8Args a) {
   using C = Keep<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -246,13 +258,12 @@ __global__ void __launch_bounds__(Keep<NT>::kThreads, 1)
     unsigned n = 0;
     for (int m = first; m < tiles && ok; m += step, ++n) {
       const unsigned acc = n & 1u;
-      const int t = m * kBM + r;
       const float snext = scale_of(m + step);
       ok = wait_or_flag(bar(C::B_TFULL + acc), (n / 2) & 1u, abort_flag, a.status) && !*abort_flag;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      __nv_bfloat16* drow = d.base + static_cast<size_t>(t) * d.ld + c0;
+      const uint32_t out = sbase + C::kOffOut + static_cast<uint32_t>(warp - 2) * 2048u;
 #pragma unroll 1
       for (int c = 0; c < C::kCols; c += 32) {
         uint32_t v[32], w[16];
@@ -265,10 +276,24 @@ __global__ void __launch_bounds__(Keep<NT>::kThreads, 1)
           if (lane == 0) mbar_arrive(bar(C::B_TEMPTY + acc));
         }
         outputs32(v, sx, s_sw + c0 + c, s_sw + NT + c0 + c, a.act, w);
-        if (t < a.T) store_row32(drow + c, w, a.vec32);
+        if (lane == 0) bulk_wait_group_read0();   // the box before has been read
+        __syncwarp();
+        // a 64-byte row of the box (64-byte swizzle)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(out + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16,
+                       make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        // (rows past T inside the box are not written; a box past T is not sent)
+        if (lane == 0 && m * kBM + 32 * q4 < a.T) {
+          tma_store_2d(&tm_out.map[d.which], out, d.col + c0 + c, m * kBM + 32 * q4);
+          bulk_commit_group();
+        }
       }
       sx = snext;
     }
+    if (lane == 0) bulk_wait_group0();
     tc_fence_before();
   }
   __syncthreads();
@@ -415,7 +440,7 @@ cudaError_t configure(K kernel, int smem) {
 
 template <int NT>
 cudaError_t launch_keep(const Proj8Args& a, const CUtensorMap& tx, const CUtensorMap& tw,
-                        cudaStream_t stream) {
+                        const Proj8Outs& to, cudaStream_t stream) {
   static std::atomic<bool> configured[64];   // per device: shared-memory opt-in done
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -431,7 +456,7 @@ cudaError_t launch_keep(const Proj8Args& a, const CUtensorMap& tx, const CUtenso
   per = per < 1 ? 1 : per > tiles ? tiles : per;
   const int nk = (a.E + kBK - 1) / kBK;
   uvqk_fp8_keep<NT><<<static_cast<unsigned>(blocks) * per, Keep<NT>::kThreads, Keep<NT>::smem(nk),
-                      stream>>>(tx, tw, a);
+                      stream>>>(tx, tw, to, a);
   return cudaGetLastError();
 }
 
@@ -470,14 +495,14 @@ int uvqk_fp8_cols(int T, int E, int N) {
 }
 
 cudaError_t launch_uvqk_fp8_sm100(const Proj8Args& a, const CUtensorMap& tx, const CUtensorMap& tw,
-                                  cudaStream_t stream) {
+                                  const Proj8Outs& to, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
   if ((a.E + kBK - 1) / kBK > kMaxW / (128 * kBK)) return launch_stream(a, tx, tw, stream);
   switch (uvqk_fp8_cols(a.T, a.E, 2 * a.Nu + 2 * a.Nq)) {
-    case 256: return launch_keep<256>(a, tx, tw, stream);
-    case 128: return launch_keep<128>(a, tx, tw, stream);
-    case 64: return launch_keep<64>(a, tx, tw, stream);
-    default: return launch_keep<32>(a, tx, tw, stream);
+    case 256: return launch_keep<256>(a, tx, tw, to, stream);
+    case 128: return launch_keep<128>(a, tx, tw, to, stream);
+    case 64: return launch_keep<64>(a, tx, tw, to, stream);
+    default: return launch_keep<32>(a, tx, tw, to, stream);
   }
 }
 
