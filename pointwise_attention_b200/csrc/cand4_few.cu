@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(1024) hstu_cand4_finish(const __grid_constant_
   const int b = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.max_cands));
   const int i = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.max_cands));
   const User us = user_ranges(a, b);
-  const int share = cut.many ? 0 : share_of(a, cut);
-  if (!us.ok || (!cut.many && !in_shares(us, share, cut))) {
+  const int share = share_of(a, cut);
+  if (!us.ok || !in_shares(us, share, cut)) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadOffsets);
     return;
   }
@@ -515,24 +515,15 @@ __global__ void __launch_bounds__(1024) hstu_cand4_finish(const __grid_constant_
   }
   const float inv_n = 1.0f / static_cast<float>(a.norm_len > 0 ? a.norm_len : us.nb + 1);
   // where the slices are, how far apart and how many
-  int slices;
-  size_t stride;
-  const float* src;
-  if (cut.many) {
-    stride = static_cast<size_t>(a.C) * D;
-    src = a.part + at;
-    slices = (us.nb + cut.chunk - 1) / cut.chunk;
-  } else {
-    // pieces of the CTAs whose shares cover the history; of a piece's parts
-    // those that have a 16-key block
-    const int c0 = us.s / share, c1 = us.nb > 0 ? (us.s + us.nb - 1) / share : c0;
-    stride = static_cast<size_t>(a.max_cands) * D;
-    src = a.part + ((static_cast<size_t>(c0) + b) * cut.parts * a.max_cands + i) * D + col;
-    slices = us.nb > 0 ? (c1 - c0 + 1) * cut.parts : 0;
-  }
+  // (pieces of the CTAs whose shares cover the history; of a piece's parts
+  // those that have a 16-key block)
+  const int c0 = us.s / share, c1 = us.nb > 0 ? (us.s + us.nb - 1) / share : c0;
+  const size_t stride = static_cast<size_t>(a.max_cands) * D;
+  const float* src = a.part + ((static_cast<size_t>(c0) + b) * cut.parts * a.max_cands + i) * D + col;
+  const int slices = us.nb > 0 ? (c1 - c0 + 1) * cut.parts : 0;
   // whether slice s was written
   auto written = [&](int s) {
-    if (cut.many || cut.parts == 1) return true;
+    if (cut.parts == 1) return true;
     const int64_t lo = static_cast<int64_t>(us.s / share + s / cut.parts) * share;
     const int64_t first = lo > us.s ? lo : us.s;
     const int64_t last = lo + share < us.s + us.nb ? lo + share : us.s + us.nb;
@@ -592,13 +583,129 @@ __global__ void __launch_bounds__(1024) hstu_cand4_finish(const __grid_constant_
       make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
 }
 
+// The same for many candidates: a warp per candidate, which keeps its whole row
+// (NH >= H heads, four dimensions of each per lane) in registers.
+template <int NH, bool POS, bool TIME>
+__global__ void __launch_bounds__(256) hstu_cand4_finish_rows(const __grid_constant__ Cand4Args a,
+                                                              const Cand4Cut cut) {
+  const int blocks = (a.max_cands + 7) / 8;
+  const int b = static_cast<int>(blockIdx.x / static_cast<unsigned>(blocks));
+  const int i = 8 * static_cast<int>(blockIdx.x % static_cast<unsigned>(blocks)) +
+                static_cast<int>(threadIdx.x >> 5);
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const User us = user_ranges(a, b);
+  if (!us.ok) {
+    if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadOffsets);
+    return;
+  }
+  if (i >= us.cb) return;
+  const int D = a.H * 128;
+  const size_t cand = checked(a.status, us.c0 + i, a.C, BS_CAND4_ROW);
+  const size_t at = cand * D + 4 * lane;     // head h: + 128 h
+  // (heads past H read nothing and count as zeros: no branch stands between the
+  // loads of different heads)
+  auto row2 = [&](const void* p, int h) {
+    return h < a.H ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at + 128 * h))
+                   : make_uint2(0u, 0u);
+  };
+  float self[NH];
+  {
+    uint2 q[NH], k[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      q[h] = row2(a.q, h);
+      k[h] = row2(a.k, h);
+    }
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      float x = fmaf(bf16_lo(q[h].x), bf16_lo(k[h].x),
+                     fmaf(bf16_hi(q[h].x), bf16_hi(k[h].x),
+                          fmaf(bf16_lo(q[h].y), bf16_lo(k[h].y), bf16_hi(q[h].y) * bf16_hi(k[h].y))));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (POS && h < a.H)
+        x += __ldg(a.rab_pos + static_cast<size_t>(h) * (2 * static_cast<size_t>(a.L) - 1) + (a.L - 1));
+      if (TIME && h < a.H) x += __ldg(a.rab_time + h * a.nb);   // time difference 0: bucket 0
+      self[h] = silu_f(x);
+    }
+  }
+  const float inv_n = 1.0f / static_cast<float>(a.norm_len > 0 ? a.norm_len : us.nb + 1);
+  const int slices = (us.nb + cut.chunk - 1) / cut.chunk;
+  const size_t stride = static_cast<size_t>(a.C) * D;
+  uint2 v[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) v[h] = row2(a.v, h);
+  grid_wait();
+  float4 o[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < slices; ++s) {
+    const float* src = a.part + s * stride + at;
+    float4 f[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+      f[h] = h < a.H ? *reinterpret_cast<const float4*>(src + 128 * h) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      o[h].x += f[h].x;
+      o[h].y += f[h].y;
+      o[h].z += f[h].z;
+      o[h].w += f[h].w;
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    o[h].x = fmaf(self[h], bf16_lo(v[h].x), o[h].x) * inv_n;
+    o[h].y = fmaf(self[h], bf16_hi(v[h].x), o[h].y) * inv_n;
+    o[h].z = fmaf(self[h], bf16_lo(v[h].y), o[h].z) * inv_n;
+    o[h].w = fmaf(self[h], bf16_hi(v[h].y), o[h].w) * inv_n;
+    sum += (o[h].x + o[h].y) + (o[h].z + o[h].w);
+  }
+  uint2 u[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) u[h] = row2(a.u, h);
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
+  const float mean = sum / static_cast<float>(D);
+  float sq = 0.f;
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    o[h].x -= mean;
+    o[h].y -= mean;
+    o[h].z -= mean;
+    o[h].w -= mean;
+    const float q = fmaf(o[h].x, o[h].x, fmaf(o[h].y, o[h].y, fmaf(o[h].z, o[h].z, o[h].w * o[h].w)));
+    sq += h < a.H ? q : 0.f;
+  }
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, e);
+  const float rstd = 1.0f / sqrtf(sq / static_cast<float>(D) + a.eps);
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    if (h >= a.H) break;
+    const float g[4] = {bf16_lo(u[h].x), bf16_hi(u[h].x), bf16_lo(u[h].y), bf16_hi(u[h].y)};
+    const float z[4] = {o[h].x * rstd, o[h].y * rstd, o[h].z * rstd, o[h].w * rstd};
+    const int col = 128 * h + 4 * lane;
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w = a.ln_weight ? __ldg(a.ln_weight + col + e) : 1.f;
+      const float c = a.ln_bias ? __ldg(a.ln_bias + col + e) : 0.f;
+      y[e] = fmaf(z[e], w, c) * silu_f(g[e]);
+    }
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + at + 128 * h) =
+        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  }
+}
+
 template <bool POS, bool TIME>
 cudaError_t launch_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_sums,
                           cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.max_cands));
   // few candidates have many slices and the SMs to themselves
-  const int groups = cut.many ? 1 : a.H <= 4 ? 8 : 32 / a.H;
+  const int groups = a.H <= 4 ? 8 : 32 / a.H;
   cfg.blockDim = dim3(32 * static_cast<unsigned>(a.H * groups));
   cfg.stream = stream;
   // launched while the kernel of the sums runs; waits for it before reading
@@ -609,6 +716,12 @@ cudaError_t launch_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_su
   attr[0].val.programmaticStreamSerializationAllowed = after_sums ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cut.many) {
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ((static_cast<unsigned>(a.max_cands) + 7) / 8));
+    cfg.blockDim = dim3(256);
+    return a.H <= 8 ? cudaLaunchKernelEx(&cfg, hstu_cand4_finish_rows<8, POS, TIME>, a, cut)
+                    : cudaLaunchKernelEx(&cfg, hstu_cand4_finish_rows<16, POS, TIME>, a, cut);
+  }
   return cudaLaunchKernelEx(&cfg, hstu_cand4_finish<POS, TIME>, a, cut, groups);
 }
 

@@ -502,10 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld_dep(ov);
         if (row_ok) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(dst + 32 * cc)[i] =
-                make_float4(__uint_as_float(ov[4 * i]), __uint_as_float(ov[4 * i + 1]),
-                            __uint_as_float(ov[4 * i + 2]), __uint_as_float(ov[4 * i + 3]));
+          for (int i = 0; i < 4; ++i)   // whole 32-byte sectors
+            st_global_v8(dst + 32 * cc + 8 * i, reinterpret_cast<const uint32_t(&)[8]>(ov[8 * i]));
         }
       }
     }
