@@ -424,15 +424,16 @@ def _arg(t, name, dtype, *shape):
     """Placement, layout, type and shape of one argument (None passes); its address."""
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()
+            and (not shape or t.shape == shape)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor (the library runs on the GPU only)" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     if t.dtype != dtype:
         raise ValueError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
-    if shape and t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    return t.data_ptr()
+    raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
 
 
 def _on(ref, *tensors):
@@ -474,23 +475,31 @@ def hstu_rmsnorm_fwd(x, *, residual=None, weight=None, eps: float = 1e-6, quant:
     rp = _arg(residual, "residual", x.dtype, T, E)
     wp = _arg(weight, "weight", _F32, E)
     h = y = q8 = scale = rstd = None
+    hp = yp = qp = sp = np_ = None
     if out is not None:
         h, y, q8, scale, rstd = (out.get(n) for n in ("h", "y", "q8", "scale", "rstd"))
-    with _on(x, residual, weight, h, y, q8, scale, rstd):
+        hp, yp = _arg(h, "h", x.dtype, T, E), _arg(y, "y", x.dtype, T, E)
+        qp, sp = _arg(q8, "q8", _F8, T, E), _arg(scale, "scale", _F32, T)
+        np_ = _arg(rstd, "rstd", _F32, T)
+        _on(x, h, y, q8, scale, rstd)
+    with _on(x, residual, weight):
         if residual is not None and h is None:
             h = torch.empty_like(x)
+            hp = h.data_ptr()
         if quant:
             if q8 is None:
                 q8 = torch.empty_like(x, dtype=_F8)
+                qp = q8.data_ptr()
             if scale is None:
                 scale = x.new_empty(T, dtype=_F32)
+                sp = scale.data_ptr()
         elif y is None:
             y = torch.empty_like(x)
+            yp = y.data_ptr()
         if save_rstd and rstd is None:
             rstd = x.new_empty(T, dtype=_F32)
-        rc = lib.hstu_rmsnorm_fwd(dt, T, E, xp, rp, wp, eps, _arg(h, "h", x.dtype, T, E),
-                                  _arg(y, "y", x.dtype, T, E), _arg(q8, "q8", _F8, T, E),
-                                  _arg(scale, "scale", _F32, T), _arg(rstd, "rstd", _F32, T),
+            np_ = rstd.data_ptr()
+        rc = lib.hstu_rmsnorm_fwd(dt, T, E, xp, rp, wp, eps, hp, yp, qp, sp, np_,
                                   _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rmsnorm_fwd")
@@ -506,17 +515,21 @@ def hstu_rmsnorm_bwd(dy, h, rstd, *, weight=None, d_residual=None, need_weight_g
     T, E = dy.shape
     args = (_arg(dy, "dy", dy.dtype), _arg(h, "h", dy.dtype, T, E), _arg(rstd, "rstd", _F32, T),
             _arg(weight, "weight", _F32, E), _arg(d_residual, "d_residual", dy.dtype, T, E))
+    dxp = _arg(dx, "dx", dy.dtype, T, E)
     with _on(dy, h, rstd, weight, d_residual, dx, workspace):
         if dx is None:
             dx = torch.empty_like(dy)
+            dxp = dx.data_ptr()
         dw, wp, wn = None, None, 0
         if need_weight_grad:
             dw = dy.new_empty(E, dtype=_F32)
             if workspace is None:
-                workspace = dy.new_empty(max(lib.hstu_rmsnorm_bwd_workspace_size(T, E), 256),
-                                         dtype=_U8)
-            workspace, wp, wn = _room(workspace, dy)
-        rc = lib.hstu_rmsnorm_bwd(dt, T, E, *args, _arg(dx, "dx", dy.dtype, T, E),
+                wn = max(lib.hstu_rmsnorm_bwd_workspace_size(T, E), 256)
+                workspace = dy.new_empty(wn, dtype=_U8)
+                wp = workspace.data_ptr()
+            else:
+                workspace, wp, wn = _room(workspace, dy)
+        rc = lib.hstu_rmsnorm_bwd(dt, T, E, *args, dxp,
                                   None if dw is None else dw.data_ptr(), wp, wn,
                                   _stream_of(dy, stream))
     if rc != HSTU_OK:
@@ -552,16 +565,19 @@ def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: 
     N = 2 * H * (d_qk + d_v)
     args = (xp, _arg(x_scale, "x_scale", _F32, T), _arg(w8, "w8", _F8, N, E),
             _arg(w_scale, "w_scale", _F32, N), _arg(bias, "bias", _F32, N))
+    shapes = (T, H * d_v), (T, H, d_v), (T, H, d_qk), (T, H, d_qk)
+    if out is not None:
+        outs = out["u"], out["v"], out["q"], out["k"]
+        ptrs = [_arg(t, n, _BF16, *sh) for t, n, sh in zip(outs, "uvqk", shapes)]
+        _on(x8, *outs)
     with _on(x8, x_scale, w8, w_scale, bias, workspace):
         if out is None:
-            new = lambda *s: x8.new_empty(s, dtype=_BF16)
-            out = dict(u=new(T, H * d_v), v=new(T, H, d_v), q=new(T, H, d_qk), k=new(T, H, d_qk))
-        u, v, q, k = out["u"], out["v"], out["q"], out["k"]
-        _on(x8, u, v, q, k)
+            u, v, q, k = (x8.new_empty(sh, dtype=_BF16) for sh in shapes)
+            out = dict(u=u, v=v, q=q, k=k)
+            ptrs = u.data_ptr(), v.data_ptr(), q.data_ptr(), k.data_ptr()
         workspace, wp, wn = _room(workspace, x8)
-        rc = lib.hstu_uvqk_fp8_fwd(T, E, H, d_qk, d_v, act, *args, _arg(u, "u", _BF16, T, H * d_v),
-                                   _arg(v, "v", _BF16, T, H, d_v), _arg(q, "q", _BF16, T, H, d_qk),
-                                   _arg(k, "k", _BF16, T, H, d_qk), wp, wn, _stream_of(x8, stream))
+        rc = lib.hstu_uvqk_fp8_fwd(T, E, H, d_qk, d_v, act, *args, *ptrs, wp, wn,
+                                   _stream_of(x8, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_uvqk_fp8_fwd")
     return out
@@ -599,9 +615,10 @@ def hstu_rab_bucket_fwd(table, length: int, thresholds, *, out=None, stream=None
     with _on(table, out):
         if out is None:
             out = table.new_empty((H, 2 * length - 1))
-        rc = lib.hstu_rab_bucket_fwd(H, length, NB, thr, tp,
-                                     _arg(out, "out", _F32, H, 2 * length - 1),
-                                     _stream_of(table, stream))
+            op = out.data_ptr()
+        else:
+            op = _arg(out, "out", _F32, H, 2 * length - 1)
+        rc = lib.hstu_rab_bucket_fwd(H, length, NB, thr, tp, op, _stream_of(table, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rab_bucket_fwd")
     return out
@@ -649,7 +666,8 @@ def hstu_kv4_pack(k, v, *, cache=None, rows=None, workspace=None, stream=None):
     ``rows`` (int32 [T], distinct, -1 skips), else to rows 0..T-1.  Without
     ``cache`` a new one of T rows.  Returns the cache."""
     lib = load_library()
-    kp = _arg(k, "k", _BF16)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [T, H, 128] tensor")
     T, H = k.shape[0], k.shape[1]
     kp, vp = _arg(k, "k", _BF16, T, H, 128), _arg(v, "v", _BF16, T, H, 128)
     rp = _arg(rows, "rows", _I32, T)

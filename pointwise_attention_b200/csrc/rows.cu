@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
 }
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 512 / block_threads<TPR>() : 1)
+__global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / block_threads<TPR>() : 1)
     hstu_rows_bwd(const RowsBwdArgs a) {
   constexpr int kRows = block_threads<TPR>() / TPR;
   constexpr int N = NV * VEC, P = N / 2;
@@ -318,44 +318,39 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 512 / b
     load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.h) + at, lane, a.E, ph);
     rn = __ldg(a.rstd + row);
   };
-  // the next row's dy and h are loaded before this row's sum is waited for,
-  // and this row's d_residual while it is added up
-  // (wider rows have enough loads in flight, and no registers to spare)
-  constexpr bool kAhead = N <= 16;
-  if (kAhead && t < a.T) load(t);
   for (; t < a.T; t += stride) {
     const size_t at = static_cast<size_t>(t) * a.E;
-    if (!kAhead) load(t);
+    load(t);
     if (a.dres) load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.dres) + at, lane, a.E, pr);
     const float r = rn;
     const uint64_t r2 = pack_f32x2(r, r);
-    // g = w dy and z = h r: dx = r g - z (r mean(g z)), dw += dy z
-    uint64_t g[P], z[P], dot2 = 0ull;
+    // g = w dy and z = h r: dx = r g - z (r mean(g z)), dw += dy z; g and z are
+    // made twice, which leaves registers for more rows on an SM
+    uint64_t dot2 = 0ull;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const uint64_t d = get_pair<T, VEC, NV>(pd, i);
-      z[i] = fmul2(get_pair<T, VEC, NV>(ph, i), r2);
-      g[i] = fmul2(d, w[i]);
-      dot2 = ffma2(g[i], z[i], dot2);
-      dw2[i] = ffma2(d, z[i], dw2[i]);
+      const uint64_t z = fmul2(get_pair<T, VEC, NV>(ph, i), r2);
+      dot2 = ffma2(fmul2(d, w[i]), z, dot2);
+      dw2[i] = ffma2(d, z, dw2[i]);
     }
-    if (kAhead && t < a.T - stride) load(t + stride);
     const float2 d2 = unpack_f32x2(dot2);
     const float dot = row_sum<TPR>(d2.x + d2.y, red);
     const float k = -r * (dot / static_cast<float>(a.E));
     const uint64_t k2 = pack_f32x2(k, k);
     T* dx = static_cast<T*>(a.dx) + at;
-    Pack<T, VEC> o[NV];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      uint64_t x = ffma2(z[i], k2, fmul2(g[i], r2));
+      const uint64_t g = fmul2(get_pair<T, VEC, NV>(pd, i), w[i]);
+      const uint64_t z = fmul2(get_pair<T, VEC, NV>(ph, i), r2);
+      uint64_t x = ffma2(z, k2, fmul2(g, r2));
       if (a.dres) x = fadd2(x, get_pair<T, VEC, NV>(pr, i));
-      put_pair<T, VEC, NV>(o, i, x);
+      put_pair<T, VEC, NV>(pd, i, x);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * VEC;
-      if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(dx + c) = o[i];
+      if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(dx + c) = pd[i];
     }
   }
   float dw[N];
