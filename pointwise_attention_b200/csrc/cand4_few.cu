@@ -139,12 +139,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   const int hg = static_cast<int>(blockIdx.x) % cut.hgroups, cta = static_cast<int>(blockIdx.x) / cut.hgroups;
   const int share = share_of(a, cut);
   const int64_t begin = static_cast<int64_t>(cta) * share, end = begin + share;
-  // the last user that starts at or before the share's first token
-  int b = 0;
-  for (int n = a.B; n > 1;) {
-    const int half = n / 2;
+  // The last user that starts at or before the share's first token: by
+  // bisection down to 256 users, then all threads look at one each (a chain of
+  // loads costs half a microsecond a link).
+  int b = 0, among = a.B;
+  while (among > kThreads) {
+    const int half = among / 2;
     if (__ldg(a.offsets + b + half) <= begin) b += half;
-    n -= half;
+    among -= half;
+  }
+  {
+    const int i = static_cast<int>(threadIdx.x);
+    const int n = __syncthreads_count(i > 0 && i < among && __ldg(a.offsets + b + i) <= begin);
+    b += n;
   }
   const int h = 8 * hg + warp % cut.heads, part = warp / cut.heads;
   const int step = 16 * cut.parts;

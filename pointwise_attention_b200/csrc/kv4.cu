@@ -31,7 +31,7 @@ namespace hstu {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWords = 4;   // words of a thread, kThreads apart: that many loads in flight
+constexpr int kWords = 8;   // words of a thread, kThreads apart: that many loads in flight
 
 struct Kv4Args {
   const void* src[2];    // pack: k, v bf16 [T, H, 128]; unpack: codes

@@ -44,7 +44,9 @@ __device__ __forceinline__ uint32_t kv4_pair(uint32_t word, uint32_t s2) {
 template <int I>
 __device__ __forceinline__ uint32_t kv4_pair_fma(uint32_t word, uint32_t s2, uint32_t m24s) {
   const uint32_t w = I == 0 ? word << 3 : word >> (I == 0 ? 0 : 4 * I - 3);
-  return hfma2((w & 0x00780078u) | 0x41804180u, s2, m24s);
+  uint32_t c;   // (w & mask) | 16.0 in one operation
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(c) : "r"(w), "r"(0x00780078u), "r"(0x41804180u));
+  return hfma2(c, s2, m24s);
 }
 __device__ __forceinline__ uint32_t kv4_m24(uint32_t s2) { return hmul2(s2, 0xC1C0C1C0u); }
 
