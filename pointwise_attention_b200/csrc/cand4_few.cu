@@ -23,7 +23,10 @@
 //   V: lane (g, t) holds dims 16g.. of keys 2t, 2t+1, 2t+8, 2t+9.
 // The candidates are the MMA's 8 columns: with few of them the tensor core's
 // work is small beside decoding and the cache's bytes, which bound the kernel.
-// P is rounded to bf16 for the second product; scores, SiLU and sums are fp32.
+// P enters the second product as the sum of two bf16 numbers (2^-16 of it is
+// lost; one number would lose 2^-8, as much as the output's own rounding, to
+// save eight of 24 MMAs that do not bound the kernel); scores, SiLU and sums
+// are fp32.
 //
 // The pieces' sums go to the workspace in fp32; a second kernel adds them in
 // order (the result does not depend on timing), adds the self term and applies
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         }
       }
       // P: keys g, g + 8 by candidates 2t, 2t+1, transposed into the B operand
-      uint32_t pb[NT][2];
+      uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -409,8 +412,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             x0 += rt[k2 & 0x7Fu];
             x1 += rt[(k2 >> 8) & 0x7Fu];
           }
-          const uint32_t p2 = pack_bf16x2(silu_f(x0), silu_f(x1));
-          pb[n][i] = transpose8(g + 8 * i < left ? p2 : 0u);
+          const bool in = g + 8 * i < left;
+          const float p0 = in ? silu_f(x0) : 0.f, p1 = in ? silu_f(x1) : 0.f;
+          const uint32_t hi = pack_bf16x2(p0, p1);
+          pb[n][i] = transpose8(hi);
+          pl[n][i] = transpose8(pack_bf16x2(p0 - bf16_lo(hi), p1 - bf16_hi(hi)));
         }
       }
       left -= step;
@@ -431,8 +437,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     {                                                                                      \
       const uint32_t a0 = kv4_pair_fma<I>(ea, sa, ma), a1 = kv4_pair_fma<I>(oa, sa, ma);   \
       const uint32_t a2 = kv4_pair_fma<I>(eb, sb, mb), a3 = kv4_pair_fma<I>(ob, sb, mb);   \
-      _Pragma("unroll") for (int n = 0; n < NT; ++n)                                       \
-          mma_16816(o[n][4 * w + I], a0, a1, a2, a3, pb[n][0], pb[n][1]);                  \
+      _Pragma("unroll") for (int n = 0; n < NT; ++n) {                                     \
+        mma_16816(o[n][4 * w + I], a0, a1, a2, a3, pb[n][0], pb[n][1]);                    \
+        mma_16816(o[n][4 * w + I], a0, a1, a2, a3, pl[n][0], pl[n][1]);                  \
+    }                                                                                    \
     }
           HSTU_PV(0)
           HSTU_PV(1)

@@ -3,17 +3,22 @@
 // memory.  cand4_few.cu states the operation; the sums that leave here are
 // finished by the same last kernel.
 //
-// A CTA takes (user, 256 candidates, head, up to `chunk` keys): two tiles of
-// 128 candidates share every decoded tile of 128 keys and values, which halves
-// the decoding, and fill TMEM: S0, S1, O0, O1 at 128 columns each.
-//   warps 0..3    decode K (warps 4..7: V): codes and scales from the cache, a
+// An item of work is (user, 256 candidates, head, up to `chunk` keys): two tiles
+// of 128 candidates share every decoded tile of 128 keys and values, which
+// halves the decoding, and fill TMEM: S0, S1, O0, O1 at 128 columns each.  A CTA
+// per SM walks the items, longest histories first, rounds in alternating
+// direction (so that each CTA's sum is about the same); the roles run on into
+// the next item on their own, so that its first tiles are decoded and
+// multiplied while the last one's sums are written (with a CTA per item a fifth
+// of the time went to starts and ends).
+//   warps 0..3    decode K (warps 4..6: V): codes and scales from the cache, a
 //                 tile ahead in registers, to bf16 in the 128-byte-swizzled
 //                 layout of the MMA operands, two stages each; the keys'
 //                 position bias and timestamps beside K
 //   warps 8..15   epilogue, four per candidate tile, a row (TMEM lane) per
 //                 thread: half bias and SiLU in fp32, P (bf16, its one
 //                 rounding) over S in TMEM; then O
-//   warp 16       TMEM, the candidates' Q by TMA, and every MMA: while one
+//   warp 7        TMEM, the candidates' Q by TMA, and every MMA: while one
 //                 tile's scores are in the epilogue, the tensor core works for
 //                 the other
 // SiLU(x) = h (1 + tanh h), h = x / 2, with tanh.approx.f32 (one special
@@ -33,11 +38,14 @@
 namespace hstu {
 namespace {
 
-constexpr int kDecWarps = 4;               // of K, and as many of V
-constexpr int kEpi0 = 2 * kDecWarps;       // first epilogue warp
+// Sixteen warps, four to a scheduler: one more would cost every thread 32
+// registers (a scheduler's share of the register file).
+constexpr int kKWarps = 4, kVWarps = 3;    // that decode K and V
+constexpr int kMmaWarp = kKWarps + kVWarps;
+constexpr int kEpi0 = kMmaWarp + 1;        // first epilogue warp
 constexpr int kEpiWarps = 8;
-constexpr int kMmaWarp = kEpi0 + kEpiWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
+constexpr int kRuns = 16;                  // a tile's rows in groups of eight
 constexpr int kHalf = 16384;               // 128 rows x 64 bf16
 constexpr int kTile = 2 * kHalf;           // 128 x 128 bf16
 constexpr int kRing = 4;                   // key metadata of this many tiles
@@ -50,8 +58,9 @@ constexpr int kOffPos = kOffV + 2 * kTile;             // float [kRing][128]: ha
 constexpr int kOffTs = kOffPos + kRing * 128 * 4;      // uint32 [kRing][128]: timestamps, low words
 constexpr int kOffThr = kOffTs + kRing * 128 * 4;      // long long [kThrLen]
 constexpr int kOffFirst = kOffThr + kThrLen * 8;       // signed char [64]
-constexpr int kOffRabH = kOffFirst + 64;               // float [kMaxBuckets]: half time bias
-constexpr int kOffOct = kOffRabH + kMaxBuckets * 4;    // uint4 [32]
+constexpr int kOffRabH = kOffFirst + 64;               // float [16][kMaxBuckets]: half time bias
+constexpr int kOffOrder = kOffRabH + 16 * kMaxBuckets * 4;   // int [kMaxOrder]: users by length
+constexpr int kOffOct = kOffOrder + kMaxOrder * 4;     // uint4 [32]
 constexpr int kOffThr32 = kOffOct + 32 * 16;           // unsigned [kMaxBuckets]
 constexpr int kOffBar = kOffThr32 + kMaxBuckets * 4;
 enum {
@@ -64,7 +73,9 @@ enum {
   B_PFULL = 12,
   B_PVDONE = 14,
   B_OFULL = 16,
-  B_META = 17,     // + ring slot
+  B_OEMPTY = 17,
+  B_END = 18,
+  B_META = 19,     // + ring slot
   kNumBars = B_META + kRing
 };
 constexpr int kOffMisc = kOffBar + kNumBars * 8;       // [0] TMEM base, [1] abort, [2] user
@@ -166,64 +177,78 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // (candidate batch, split, head, rank of the user), batches fastest: the
-  // batches of one (user, head) share its cache rows in L2; long histories first
-  unsigned x = blockIdx.x;
-  const unsigned batches = (static_cast<unsigned>(a.max_cands) + 255u) / 256u;
-  const int mb = static_cast<int>(x % batches);
-  x /= batches;
-  const int split = static_cast<int>(x % static_cast<unsigned>(a.splits));
-  x /= static_cast<unsigned>(a.splits);
-  const int h = static_cast<int>(x % static_cast<unsigned>(a.H));
-  const int rank = static_cast<int>(x / static_cast<unsigned>(a.H));
-  int b = rank;
-  if (a.B > 1 && a.B <= kMaxOrder) {
-    // the user of this rank (ties by index): every thread ranks one user
+  int* order = reinterpret_cast<int*>(smem + kOffOrder);
+  const bool ordered = a.B > 1 && a.B <= kMaxOrder;
+  if (ordered) {
+    // the users by history length, longest first (ties by index)
     int* len = reinterpret_cast<int*>(smem + kOffPos);   // before its ring is in use
-    for (int i = threadIdx.x; i < a.B; i += kThreads)
+    for (int i = threadIdx.x; i < a.B; i += kThreads) {
       len[i] = __ldg(a.offsets + i + 1) - __ldg(a.offsets + i);
-    if (threadIdx.x == 0) misc[2] = 0;
+      order[i] = i;   // (in range whatever the offsets are)
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < a.B; i += kThreads) {
       const int n = len[i];
       int r = 0;
       for (int o = 0; o < a.B; ++o) r += (len[o] > n || (len[o] == n && o < i)) ? 1 : 0;
-      if (r == rank) misc[2] = static_cast<uint32_t>(i);
+      order[r] = i;
     }
-    __syncthreads();
-    b = static_cast<int>(misc[2]);
   }
-  const int c0 = __ldg(a.cand_offsets + b);
-  const int cb = __ldg(a.cand_offsets + b + 1) - c0;
-  const int s = __ldg(a.offsets + b);
-  const int nb = __ldg(a.offsets + b + 1) - s;
-  const int r0 = a.first_rows ? __ldg(a.first_rows + b) : s;
-  if (c0 < 0 || cb < 0 || cb > a.C - c0 || cb > a.max_cands || s < 0 || nb < 0 || nb > a.T - s ||
-      nb > a.max_seq_len || r0 < 0 || nb > a.R - r0 || (POS && nb >= a.L)) {
-    if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadOffsets);
-    return;
-  }
-  const int key0 = split * a.chunk;
-  const int keys = min(nb - key0, a.chunk);              // this CTA's
-  const int rows = min(cb - 256 * mb, 256);
-  if (rows <= 0 || keys <= 0) return;
-  const int cand0 = c0 + 256 * mb;
-  const int nt = (keys + 127) / 128;
-  const int tiles = rows > 128 ? 2 : 1;                  // candidate tiles
+  const unsigned batches = (static_cast<unsigned>(a.max_cands) + 255u) / 256u;
+  const unsigned items = batches * static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.H) *
+                         static_cast<unsigned>(a.B);
+  // The CTA's item of each round, and what it is: (candidate batch, split, head,
+  // rank of the user), batches fastest: the batches of one (user, head) run at
+  // the same time and share its cache rows in L2.
+  struct Item {
+    int h, c0, cand0, rows, s, nb, r0, split, key0, keys, nt, tiles;
+  };
+  auto item_of = [&](unsigned round, Item& it) {   // false: nothing to do
+    const unsigned base = round * gridDim.x;
+    unsigned x = base + ((round & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+    if (x >= items) return false;
+    const int mb = static_cast<int>(x % batches);
+    x /= batches;
+    it.split = static_cast<int>(x % static_cast<unsigned>(a.splits));
+    x /= static_cast<unsigned>(a.splits);
+    it.h = static_cast<int>(x % static_cast<unsigned>(a.H));
+    const int rank = static_cast<int>(x / static_cast<unsigned>(a.H));
+    const int b = ordered ? order[rank] : rank;
+    it.c0 = __ldg(a.cand_offsets + b);
+    const int cb = __ldg(a.cand_offsets + b + 1) - it.c0;
+    it.s = __ldg(a.offsets + b);
+    it.nb = __ldg(a.offsets + b + 1) - it.s;
+    it.r0 = a.first_rows ? __ldg(a.first_rows + b) : it.s;
+    // ranges that contradict the sizes are reported by the last kernel
+    if (it.c0 < 0 || cb < 0 || cb > a.C - it.c0 || cb > a.max_cands || it.s < 0 || it.nb < 0 ||
+        it.nb > a.T - it.s || it.nb > a.max_seq_len || it.r0 < 0 || it.nb > a.R - it.r0 ||
+        (POS && it.nb >= a.L))
+      return false;
+    it.key0 = it.split * a.chunk;
+    it.keys = min(it.nb - it.key0, a.chunk);
+    it.rows = min(cb - 256 * mb, 256);
+    it.cand0 = it.c0 + 256 * mb;
+    it.nt = (it.keys + 127) / 128;
+    it.tiles = it.rows > 128 ? 2 : 1;                  // candidate tiles
+    return it.rows > 0 && it.keys > 0;
+  };
+  const unsigned rounds = (items + gridDim.x - 1u) / gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_QFULL + i), 1);
-      mbar_init(bar(B_KFULL + i), kDecWarps);
+      mbar_init(bar(B_KFULL + i), kKWarps);
       mbar_init(bar(B_KEMPTY + i), 1);
-      mbar_init(bar(B_VFULL + i), kDecWarps);
+      mbar_init(bar(B_VFULL + i), kVWarps);
       mbar_init(bar(B_VEMPTY + i), 1);
       mbar_init(bar(B_SFULL + i), 1);
       mbar_init(bar(B_PFULL + i), kEpiWarps / 2);   // the tile's epilogue warps
       mbar_init(bar(B_PVDONE + i), 1);
     }
     mbar_init(bar(B_OFULL), 1);
-    for (int i = 0; i < kRing; ++i) mbar_init(bar(B_META + i), kDecWarps);
+    mbar_init(bar(B_OEMPTY), kEpiWarps);
+    mbar_init(bar(B_END), 1);
+    for (int i = 0; i < kRing; ++i) mbar_init(bar(B_META + i), kKWarps);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -236,9 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (TIME) {
     for (int i = threadIdx.x; i < kThrLen; i += kThreads) s_thr[i] = a.bt.thr[i];
     for (int i = threadIdx.x; i < 64; i += kThreads) s_first[i] = a.bt.first_k[i];
-    for (int i = threadIdx.x; i < kMaxBuckets; i += kThreads)
-      reinterpret_cast<float*>(smem + kOffRabH)[i] =
-          i < a.nb ? 0.5f * __ldg(a.rab_time + h * a.nb + i) : 0.f;
+    for (int i = threadIdx.x; i < a.H * kMaxBuckets; i += kThreads) {
+      const int h = i / kMaxBuckets, k = i % kMaxBuckets;
+      reinterpret_cast<float*>(smem + kOffRabH)[i] = k < a.nb ? 0.5f * __ldg(a.rab_time + h * a.nb + k) : 0.f;
+    }
     for (int i = threadIdx.x; i < 32; i += kThreads)
       reinterpret_cast<uint4*>(smem + kOffOct)[i] = a.bt.oct[i];
     for (int i = threadIdx.x; i < kMaxBuckets; i += kThreads)
@@ -254,92 +280,100 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  if (warp < kEpi0) {
+  if (warp < kMmaWarp) {
     // ------------------------------------------------------------ decode
-    // lane (row, t): the row's dims 32t..32t+31; rows 8 w + 32 i + row of the tile
-    const bool is_k = warp < kDecWarps;
-    const int w = warp & (kDecWarps - 1), t = lane & 3, row = 8 * w + (lane >> 2);
+    // lane (row, t): the row's dims 32t..32t+31; rows 8 (w + warps i) + row of
+    // the tile
+    const bool is_k = warp < kKWarps;
+    const int warps = is_k ? kKWarps : kVWarps;
+    const int w = is_k ? warp : warp - kKWarps, t = lane & 3, row = 8 * w + (lane >> 2);
+    constexpr int kMost = (kRuns + kVWarps - 1) / kVWarps;
     const uint8_t* codes = is_k ? a.k_codes : a.v_codes;
     const uint16_t* scales = is_k ? a.k_scales : a.v_scales;
     const uint32_t dst = sbase + (is_k ? kOffK : kOffV);
     const int b_full = is_k ? B_KFULL : B_VFULL, b_empty = is_k ? B_KEMPTY : B_VEMPTY;
-    const float* rpos =
-        POS ? a.rab_pos + static_cast<size_t>(h) * (2 * static_cast<size_t>(a.L) - 1) + (a.L - 1) : nullptr;
-    uint4 c[4];
-    uint32_t sc[4];
+    uint4 c[kMost];
+    uint32_t sc[kMost];
     float pos = 0.f;
     uint32_t ts = 0;
+    Item it;
     auto load = [&](int n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 128 * n + 32 * i + row;
-        c[i] = make_uint4(0u, 0u, 0u, 0u);      // keys past the CTA's decode to zeros
+      for (int i = 0; i < kMost; ++i) {
+        if (w + warps * i >= kRuns) break;
+        const int key = 128 * n + 8 * warps * i + row;
+        c[i] = make_uint4(0u, 0u, 0u, 0u);      // keys past the item's decode to zeros
         sc[i] = 0u;
-        if (key < keys) {
+        if (key < it.keys) {
           const size_t at =
-              static_cast<size_t>(checked(a.status, r0 + key0 + key, a.R, BS_CAND4_KEY)) * a.H + h;
+              static_cast<size_t>(checked(a.status, it.r0 + it.key0 + key, a.R, BS_CAND4_KEY)) * a.H + it.h;
           c[i] = __ldg(reinterpret_cast<const uint4*>(codes + at * 64) + t);
           sc[i] = __ldg(scales + at * 4 + t);
         }
       }
       if (is_k) {
         const int key = 128 * n + 32 * w + lane;
-        if (POS) pos = key < keys ? __ldg(rpos + (nb - key0 - key)) : 0.f;
+        if (POS) {
+          const float* rpos = a.rab_pos + static_cast<size_t>(it.h) * (2 * static_cast<size_t>(a.L) - 1) + (a.L - 1);
+          pos = key < it.keys ? __ldg(rpos + (it.nb - it.key0 - key)) : 0.f;
+        }
         if (TIME)
           ts = static_cast<uint32_t>(__ldg(
-              a.timestamps + checked(a.status, s + key0 + min(key, keys - 1), a.T, BS_CAND4_TS)));
+              a.timestamps + checked(a.status, it.s + it.key0 + min(key, it.keys - 1), a.T, BS_CAND4_TS)));
       }
     };
-    load(0);
     bool ok = true;
-    for (int n = 0; n < nt; ++n) {
-      const int st = n & 1, use = n >> 1, slot = n & (kRing - 1);
-      if (use > 0) ok = flagged(mbar_wait(bar(b_empty + st), (use - 1) & 1, abort_flag), a.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+    unsigned tn = 0;      // tiles of all items so far
+    for (unsigned round = 0; round < rounds && ok; ++round) {
+      if (!item_of(round, it)) continue;
+      load(0);
+      for (int n = 0; n < it.nt; ++n, ++tn) {
+        const unsigned st = tn & 1u, use = tn >> 1, slot = tn & (kRing - 1);
+        if (use > 0) ok = flagged(mbar_wait(bar(b_empty + st), (use - 1) & 1, abort_flag), a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) decode_group(dst + st * kTile, row + 32 * i, t, c[i], sc[i]);
-      if (is_k) {
-        // the slot's last readers finished tile n - kRing before S of tile n - 2
-        // could be issued, which the wait above saw completed
-        if (POS) reinterpret_cast<float*>(smem + kOffPos)[slot * 128 + 32 * w + lane] = 0.5f * pos;
-        if (TIME) reinterpret_cast<uint32_t*>(smem + kOffTs)[slot * 128 + 32 * w + lane] = ts;
+        for (int i = 0; i < kMost; ++i) {
+          if (w + warps * i >= kRuns) break;
+          decode_group(dst + st * kTile, row + 8 * warps * i, t, c[i], sc[i]);
+        }
+        if (is_k) {
+          // the slot's last readers finished tile tn - kRing before S of tile
+          // tn - 2 could be issued, which the wait above saw completed
+          if (POS) reinterpret_cast<float*>(smem + kOffPos)[slot * 128 + 32 * w + lane] = 0.5f * pos;
+          if (TIME) reinterpret_cast<uint32_t*>(smem + kOffTs)[slot * 128 + 32 * w + lane] = ts;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(b_full + st));
+          if (is_k) mbar_arrive(bar(B_META + slot));
+        }
+        if (n + 1 < it.nt) load(n + 1);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(b_full + st));
-        if (is_k) mbar_arrive(bar(B_META + slot));
-      }
-      if (n + 1 < nt) load(n + 1);
     }
     if (!ok) *abort_flag = 1;
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ Q and the MMAs
     // the whole warp walks the schedule; one lane issues
-    if (elect_one()) {
-      for (int g = 0; g < tiles; ++g) {
-        const int qrow = checked(a.status, cand0 + 128 * g, a.C, BS_CAND4_ROW);
-        mbar_arrive_expect_tx(bar(B_QFULL + g), kTile);
-        tma_load_3d(sbase + kOffQ + g * kTile, &tm_q, bar(B_QFULL + g), 0, h, qrow);
-        tma_load_3d(sbase + kOffQ + g * kTile + kHalf, &tm_q, bar(B_QFULL + g), 64, h, qrow);
-      }
-    }
-    __syncwarp();
     bool ok = true;
-    auto wait = [&](int i, int parity) {
+    auto wait = [&](int i, unsigned parity) {
       if (ok)
         ok = __all_sync(0xffffffffu,
-                        flagged(mbar_wait(bar(i), parity & 1, abort_flag), a.status));
+                        flagged(mbar_wait(bar(i), parity & 1u, abort_flag), a.status));
     };
-    // S of candidate tile g and key tile n; its columns hold P of tile n - 1
-    // until that tile's P V is done
+    // so far: tiles, items, and per candidate tile its Q tiles, S and P V products
+    unsigned tn = 0, done = 0, qn[2] = {0u, 0u}, sn[2] = {0u, 0u}, pn[2] = {0u, 0u};
+    Item it;
+    // S of candidate tile g and the item's key tile n; its columns hold the P
+    // of its tile before until that one's P V is done
     auto issue_s = [&](int g, int n) {
-      const int st = n & 1;
-      if (n == 0) wait(B_QFULL + g, 0);
-      wait(B_KFULL + st, n >> 1);
-      if (n > 0) wait(B_PVDONE + g, n - 1);
+      const unsigned st = (tn + n) & 1u;
+      if (n == 0) wait(B_QFULL + g, qn[g] - 1);
+      wait(B_KFULL + st, (tn + n) >> 1);
+      if (sn[g] > 0) wait(B_PVDONE + g, sn[g] - 1);
       if (!ok) return;
+      ++sn[g];
       tc_fence_after();
       if (elect_one()) {
         const uint64_t qd = sw128_desc(sbase + kOffQ + g * kTile, 16, 1024);
@@ -349,164 +383,216 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
           mma_ss(tmem + 128u * g, qd + off, kd + off, kIdescS, ks > 0 ? 1u : 0u);
         }
-        if (g == tiles - 1) mma_commit(bar(B_KEMPTY + st));
+        if (g == it.tiles - 1) mma_commit(bar(B_KEMPTY + st));
         mma_commit(bar(B_SFULL + g));
       }
       __syncwarp();
     };
-    for (int g = 0; g < tiles; ++g) issue_s(g, 0);
-    for (int n = 0; n < nt && ok; ++n) {
-      const int st = n & 1;
-      for (int g = 0; g < tiles && ok; ++g) {
-        wait(B_VFULL + st, n >> 1);
-        wait(B_PFULL + g, n);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t vd = sw128_desc(sbase + kOffV + st * kTile, kHalf, 1024);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            // keys 16ks..16ks+15: P of a 32-column block sits in its first 16 columns
-            mma_ts(tmem + kColO + 128u * g, tmem + 128u * g + 32u * (ks >> 1) + 8u * (ks & 1),
-                   vd + ks * (2048 >> 4), kIdescPV, (n > 0 || ks > 0) ? 1u : 0u);
-          if (g == tiles - 1) mma_commit(bar(B_VEMPTY + st));
-          mma_commit(bar(B_PVDONE + g));
+    for (unsigned round = 0; round < rounds && ok; ++round) {
+      if (!item_of(round, it)) continue;
+      // the item before has no S left to compute from its Q
+      if (tn > 0) wait(B_KEMPTY + ((tn - 1) & 1u), (tn - 1) >> 1);
+      if (!ok) break;
+      if (elect_one()) {
+        for (int g = 0; g < it.tiles; ++g) {
+          const int qrow = checked(a.status, it.cand0 + 128 * g, a.C, BS_CAND4_ROW);
+          mbar_arrive_expect_tx(bar(B_QFULL + g), kTile);
+          tma_load_3d(sbase + kOffQ + g * kTile, &tm_q, bar(B_QFULL + g), 0, it.h, qrow);
+          tma_load_3d(sbase + kOffQ + g * kTile + kHalf, &tm_q, bar(B_QFULL + g), 64, it.h, qrow);
         }
-        __syncwarp();
-        if (n + 1 < nt) issue_s(g, n + 1);
       }
+      __syncwarp();
+      for (int g = 0; g < it.tiles; ++g) ++qn[g];
+      for (int g = 0; g < it.tiles; ++g) issue_s(g, 0);
+      for (int n = 0; n < it.nt && ok; ++n) {
+        const unsigned st = (tn + n) & 1u;
+        for (int g = 0; g < it.tiles && ok; ++g) {
+          wait(B_VFULL + st, (tn + n) >> 1);
+          wait(B_PFULL + g, pn[g]);
+          if (n == 0 && g == 0 && done > 0) wait(B_OEMPTY, done - 1);   // O of the item before is read
+          if (!ok) break;
+          ++pn[g];
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t vd = sw128_desc(sbase + kOffV + st * kTile, kHalf, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              // keys 16ks..16ks+15: P of a 32-column block sits in its first 16 columns
+              mma_ts(tmem + kColO + 128u * g, tmem + 128u * g + 32u * (ks >> 1) + 8u * (ks & 1),
+                     vd + ks * (2048 >> 4), kIdescPV, (n > 0 || ks > 0) ? 1u : 0u);
+            if (g == it.tiles - 1) mma_commit(bar(B_VEMPTY + st));
+            mma_commit(bar(B_PVDONE + g));
+            if (n == it.nt - 1 && g == it.tiles - 1) mma_commit(bar(B_OFULL));
+          }
+          __syncwarp();
+          if (n + 1 < it.nt) issue_s(g, n + 1);
+        }
+      }
+      tn += it.nt;
+      ++done;
     }
     if (!ok) {
       *abort_flag = 1;
       // the copies of Q land before shared memory is released
-      for (int g = 0; g < tiles; ++g) mbar_wait(bar(B_QFULL + g), 0, nullptr);
+      for (int g = 0; g < 2; ++g)
+        if (qn[g] > 0) mbar_wait(bar(B_QFULL + g), (qn[g] - 1) & 1u, nullptr);
     }
-    if (elect_one()) mma_commit(bar(B_OFULL));
+    if (elect_one()) mma_commit(bar(B_END));
     __syncwarp();
     // TMEM is released only after every MMA issued here has completed.
-    mbar_wait(bar(B_OFULL), 0, nullptr);
+    mbar_wait(bar(B_END), 0, nullptr);
   } else {
     // ------------------------------------------------------------ epilogue
     const int g = (warp - kEpi0) >> 2, q4 = warp & 3;
     const int r = 128 * g + 32 * q4 + lane;
-    const bool row_ok = r < rows;
-    const bool live = 128 * g + 32 * q4 < rows;    // the warp has candidates
-    // rows past the last candidate repeat it, so that a warp's plans are of one kind
-    const int cand = cand0 + min(r, rows - 1);
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     const uint32_t saddr = lane_addr + 128u * g;
-    const long long my_ts =
-        TIME ? __ldg(a.cand_ts + checked(a.status, cand, a.C, BS_CAND4_ROW)) : 0ll;
-    // this candidate's time plans against tile n's four blocks, loaded a tile ahead
-    uint32_t pw[4] = {0u, 0u, 0u, 0u};
-    auto load_plans = [&](int n) {
-      const uint32_t* p = a.plan + static_cast<size_t>(key0 / 32 + 4 * n) * a.C + cand;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (128 * n + 32 * i < keys) pw[i] = __ldg(p + static_cast<size_t>(i) * a.C);
-    };
-    if (TIME && live) load_plans(0);
+    const size_t D = static_cast<size_t>(a.H) * 128;
     bool ok = true;
-    for (int n = 0; n < nt && g < tiles; ++n) {
-      const int slot = n & (kRing - 1);
-      ok = flagged(mbar_wait(bar(B_SFULL + g), n & 1, abort_flag), a.status) &&
-           flagged(mbar_wait(bar(B_META + slot), (n / kRing) & 1, abort_flag), a.status);
-      ok = __all_sync(0xffffffffu, ok);   // the TMEM accesses below are warp-collective
-      if (!ok) break;
-      tc_fence_after();
-      if (live) {
+    unsigned tn = 0, done = 0, en = 0;   // tiles and items so far, this candidate tile's S
+    for (unsigned round = 0; round < rounds; ++round) {
+      // (what the tiles need of the item; the rest is looked up again, so that
+      // it holds no registers meanwhile)
+      int keys, nt, cand, rows, tiles;
+      const uint32_t* plan = nullptr;
+      {
+        Item it;
+        if (!item_of(round, it)) continue;
+        keys = it.keys;
+        nt = it.nt;
+        rows = it.rows;
+        tiles = it.tiles;
+        // rows past the last candidate repeat it, so that a warp's plans are of one kind
+        cand = it.cand0 + min(r, it.rows - 1);
+        if (TIME) plan = a.plan + static_cast<size_t>(it.key0 / 32) * a.C + cand;
+        tab.rabh_ = reinterpret_cast<const float*>(smem + kOffRabH) + it.h * kMaxBuckets;
+      }
+      const bool live = 128 * g + 32 * q4 < rows;    // the warp has candidates
+      const uint32_t my32 =
+          TIME ? static_cast<uint32_t>(__ldg(a.cand_ts + checked(a.status, cand, a.C, BS_CAND4_ROW))) : 0u;
+      // this candidate's time plans against tile n's four blocks, loaded a tile ahead
+      uint32_t pw[4] = {0u, 0u, 0u, 0u};
+      auto load_plans = [&](int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (128 * n + 32 * i < keys) pw[i] = __ldg(plan + static_cast<size_t>(i) * a.C);
+        plan += static_cast<size_t>(4) * a.C;
+      };
+      if (TIME && live) load_plans(0);
+      for (int n = 0; n < nt && g < tiles; ++n) {
+        const unsigned slot = (tn + n) & (kRing - 1);
+        ok = flagged(mbar_wait(bar(B_SFULL + g), en & 1u, abort_flag), a.status) &&
+             flagged(mbar_wait(bar(B_META + slot), ((tn + n) / kRing) & 1u, abort_flag), a.status);
+        ok = __all_sync(0xffffffffu, ok);   // the TMEM accesses below are warp-collective
+        if (!ok) break;
+        ++en;
+        tc_fence_after();
+        if (live) {
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          const int col = 32 * cc;                       // first column of the block
-          const int valid = keys - (128 * n + col);      // its keys
-          uint32_t packed[16];
-          if (valid <= 0) {
+          for (int cc = 0; cc < 4; ++cc) {
+            const int col = 32 * cc;                       // first column of the block
+            const int valid = keys - (128 * n + col);      // its keys
+            uint32_t packed[16];
+            if (valid <= 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) packed[i] = 0u;
-          } else {
-            uint32_t sv[32];
-            tmem_ld32_nowait(saddr + col, sv);
-            const float* pos = reinterpret_cast<const float*>(smem + kOffPos) + slot * 128 + col;
-            const uint32_t* ts32 = reinterpret_cast<const uint32_t*>(smem + kOffTs) + slot * 128 + col;
-            TimePlan tp{};
-            float tv[4] = {0.f, 0.f, 0.f, 0.f};
-            int tb = TB_NONE;
-            if (TIME) {
-              tb = plan_unword(tp, pw[0]);
-              // blocks come in order: the next one's word moves up
-              pw[0] = pw[1];
-              pw[1] = pw[2];
-              pw[2] = pw[3];
-              tv[0] = tab.rabt()[tp.k_a];
-              tv[1] = tab.rabt()[max(tp.k_a - 1, 0)];
-            }
-            tmem_wait_ld_dep(sv);
-            const uint32_t my32 = static_cast<uint32_t>(my_ts);
-            if (!TIME || tb == TB_NONE) {
-              p_block<POS, TB_NONE>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
-            } else if (tb == TB_CONST) {
-              p_block<POS, TB_CONST>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
-            } else if (tb == TB_SPLIT) {
-              p_block<POS, TB_SPLIT>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
-            } else if (tb == TB_MULTI) {
-              tv[2] = tab.rabt()[max(tp.k_a - 2, 0)];
-              tv[3] = tab.rabt()[max(tp.k_a - 3, 0)];
-              p_block<POS, TB_MULTI>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
-            } else if (tb == TB_GEN32) {
-              p_block<POS, TB_GEN32>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
+              for (int i = 0; i < 16; ++i) packed[i] = 0u;
             } else {
-              // time spans of 2^31 or more: the 64-bit bucket search per element
+              uint32_t sv[32];
+              tmem_ld32_nowait(saddr + col, sv);
+              const float* pos = reinterpret_cast<const float*>(smem + kOffPos) + slot * 128 + col;
+              const uint32_t* ts32 = reinterpret_cast<const uint32_t*>(smem + kOffTs) + slot * 128 + col;
+              TimePlan tp{};
+              float tv[4] = {0.f, 0.f, 0.f, 0.f};
+              int tb = TB_NONE;
+              if (TIME) {
+                tb = plan_unword(tp, pw[0]);
+                // blocks come in order: the next one's word moves up
+                pw[0] = pw[1];
+                pw[1] = pw[2];
+                pw[2] = pw[3];
+                tv[0] = tab.rabt()[tp.k_a];
+                tv[1] = tab.rabt()[max(tp.k_a - 1, 0)];
+              }
+              tmem_wait_ld_dep(sv);
+              if (!TIME || tb == TB_NONE) {
+                p_block<POS, TB_NONE>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
+              } else if (tb == TB_CONST) {
+                p_block<POS, TB_CONST>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
+              } else if (tb == TB_SPLIT) {
+                p_block<POS, TB_SPLIT>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
+              } else if (tb == TB_MULTI) {
+                tv[2] = tab.rabt()[max(tp.k_a - 2, 0)];
+                tv[3] = tab.rabt()[max(tp.k_a - 3, 0)];
+                p_block<POS, TB_MULTI>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
+              } else if (tb == TB_GEN32) {
+                p_block<POS, TB_GEN32>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
+              } else {
+                // time spans of 2^31 or more: the 64-bit bucket search per element
+                Item it;
+                item_of(round, it);
+                const long long my_ts = __ldg(a.cand_ts + cand);
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                float y[2];
+                for (int c = 0; c < 32; c += 2) {
+                  float y[2];
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                  const int key = min(key0 + 128 * n + col + c + f, nb - 1);
-                  const long long kt =
-                      __ldg(a.timestamps + checked(a.status, s + key, a.T, BS_CAND4_TS));
-                  float hx = POS ? fmaf(__uint_as_float(sv[c + f]), 0.5f, pos[c + f])
-                                 : 0.5f * __uint_as_float(sv[c + f]);
-                  hx += tab.rabt()[time_bucket(my_ts - kt, s_thr, s_first)];
-                  y[f] = fmaf(hx, tanh_approx(hx), hx);
+                  for (int f = 0; f < 2; ++f) {
+                    const int key = min(it.key0 + 128 * n + col + c + f, it.nb - 1);
+                    const long long kt =
+                        __ldg(a.timestamps + checked(a.status, it.s + key, a.T, BS_CAND4_TS));
+                    float hx = POS ? fmaf(__uint_as_float(sv[c + f]), 0.5f, pos[c + f])
+                                   : 0.5f * __uint_as_float(sv[c + f]);
+                    hx += tab.rabt()[time_bucket(my_ts - kt, s_thr, s_first)];
+                    y[f] = fmaf(hx, tanh_approx(hx), hx);
+                  }
+                  packed[c / 2] = pack_bf16x2(y[0], y[1]);
                 }
-                packed[c / 2] = pack_bf16x2(y[0], y[1]);
+              }
+              if (valid < 32) {
+                // keys past the CTA's last weigh exactly 0
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  packed[i] &= (2 * i < valid ? 0x0000FFFFu : 0u) | (2 * i + 1 < valid ? 0xFFFF0000u : 0u);
               }
             }
-            if (valid < 32) {
-              // keys past the CTA's last weigh exactly 0
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                packed[i] &= (2 * i < valid ? 0x0000FFFFu : 0u) | (2 * i + 1 < valid ? 0xFFFF0000u : 0u);
-            }
+            tmem_st16(saddr + col, packed);   // over this row's own S columns, already read
           }
-          tmem_st16(saddr + col, packed);   // over this row's own S columns, already read
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL + g));
+        if (TIME && live && n + 1 < nt) load_plans(n + 1);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_PFULL + g));
-      if (TIME && live && n + 1 < nt) load_plans(n + 1);
-    }
-    if (ok) ok = flagged(mbar_wait(bar(B_OFULL), 0, abort_flag), a.status);
-    ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
-    if (!ok && lane == 0) *abort_flag = 1;
-    if (ok && live) {
+      if (ok) ok = flagged(mbar_wait(bar(B_OFULL), done & 1u, abort_flag), a.status);
+      ok = __all_sync(0xffffffffu, ok) && !*abort_flag;
+      if (!ok) break;
+      tn += nt;
+      ++done;
       tc_fence_after();
-      const size_t D = static_cast<size_t>(a.H) * 128;
-      float* dst = a.part + (static_cast<size_t>(split) * a.C + cand) * D + h * 128;
+      Item it;
+      item_of(round, it);
+      float* dst = a.part + (static_cast<size_t>(it.split) * a.C + cand) * D + it.h * 128;
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t ov[32];
-        tmem_ld32_nowait(lane_addr + kColO + 128u * g + 32u * cc, ov);
-        tmem_wait_ld_dep(ov);
-        if (row_ok) {
+        if (live) {
+          tmem_ld32_nowait(lane_addr + kColO + 128u * g + 32u * cc, ov);
+          tmem_wait_ld_dep(ov);
+        }
+        if (cc == 3) {
+          // O is in registers: the next item's P V may have its columns
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_OEMPTY));
+        }
+        if (live && r < rows) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)   // whole 32-byte sectors
             st_global_v8(dst + 32 * cc + 8 * i, reinterpret_cast<const uint32_t(&)[8]>(ov[8 * i]));
         }
       }
     }
+    if (!ok && lane == 0) *abort_flag = 1;
     tc_fence_before();
   }
   __syncthreads();
@@ -528,9 +614,10 @@ cudaError_t launch_t(const Cand4Args& a, const CUtensorMap& tq, cudaStream_t str
     if (err != cudaSuccess) return err;
     if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
   }
-  const unsigned grid = static_cast<unsigned>((a.max_cands + 255) / 256) *
-                        static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.H) *
-                        static_cast<unsigned>(a.B);
+  const unsigned items = static_cast<unsigned>((a.max_cands + 255) / 256) *
+                         static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.H) *
+                         static_cast<unsigned>(a.B);
+  const unsigned grid = items < 148u ? items : 148u;
   hstu_cand4_sm100<POS, TIME><<<grid, kThreads, kSmem, stream>>>(tq, a);
   return cudaGetLastError();
 }

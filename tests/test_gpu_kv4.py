@@ -254,15 +254,16 @@ def test_scoring_variants(kw, cands):
     check(c, c.call(max_len=min(c.L - 1, 777), max_cands=max(cands) + 90))
 
 
-@pytest.mark.parametrize("B,most,cands", [(700, 20, 2), (300, 70, 1), (600, 40, 20)])
+@pytest.mark.parametrize("B,most,cands", [(700, 20, 2), (300, 70, 1), (600, 40, 20), (120, 300, 200)])
 def test_many_users(B, most, cands):
-    """More users than a block has threads, and than are ranked by length;
-    empty histories and users without candidates among them."""
+    """More users than a block has threads, than are ranked by length, and than
+    there are CTAs (one or two tiles of candidates each); empty histories and
+    users without candidates among them."""
     g = gen(B)
     lens = torch.randint(0, most + 1, (B,), generator=g).tolist()
     m = torch.randint(0, cands + 1, (B,), generator=g).tolist()
     m[0] = cands
-    c = Case(B, lens, m, 2, time=B == 300)
+    c = Case(B, lens, m, 4 if B == 120 else 2, time=B in (300, 120))
     check(c, c.call())
 
 
