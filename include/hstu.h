@@ -287,7 +287,8 @@ HSTU_API hstu_status_t hstu_cand_fwd(const hstu_problem_t *p, const void *k_hist
  * At least one of y and q8 is required.  h may be NULL, and is only written
  * with a residual; it may be x or residual, and y may be any of the three.
  * Sums are fp32 (a row whose sum of squares exceeds fp32 gives zeros); a row
- * that holds a NaN gives NaN.  Any E from 1 to 16384 and any alignment of
+ * that holds a NaN gives NaN.  Any E from 1 to 16384, T up to 2^31 - 2^16 (in
+ * all four calls on rows) and any alignment of
  * whole elements; E a multiple of 16 bytes with 16-byte aligned pointers (the
  * bytes of q8: 8 with bf16, 4 with fp32) takes the vector path.  No workspace.
  */

@@ -499,7 +499,7 @@ def hstu_rmsnorm_fwd(x, *, residual=None, weight=None, eps: float = 1e-6, quant:
         if save_rstd and rstd is None:
             rstd = x.new_empty(T, dtype=_F32)
             np_ = rstd.data_ptr()
-        rc = lib.hstu_rmsnorm_fwd(dt, T, E, xp, rp, wp, eps, hp, yp, qp, sp, np_,
+        rc = lib.hstu_rmsnorm_fwd(dt, T, E, xp, rp, wp, float(eps), hp, yp, qp, sp, np_,
                                   _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rmsnorm_fwd")
@@ -576,7 +576,7 @@ def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: 
             out = dict(u=u, v=v, q=q, k=k)
             ptrs = u.data_ptr(), v.data_ptr(), q.data_ptr(), k.data_ptr()
         workspace, wp, wn = _room(workspace, x8)
-        rc = lib.hstu_uvqk_fp8_fwd(T, E, H, d_qk, d_v, act, *args, *ptrs, wp, wn,
+        rc = lib.hstu_uvqk_fp8_fwd(T, E, H, d_qk, d_v, int(act), *args, *ptrs, wp, wn,
                                    _stream_of(x8, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_uvqk_fp8_fwd")
@@ -749,19 +749,23 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
     limit = (timestamps.numel() if timestamps is not None else
              R if first_rows is None else 2 ** 31 - 1)
     if offsets_host is not None:
+        if (offsets_host.is_cuda or offsets_host.dtype != _I32 or offsets_host.shape != (B + 1,)
+                or not offsets_host.is_contiguous()):
+            raise ValueError("offsets_host must be a contiguous int32 CPU tensor [B + 1]")
         total_tokens = int(offsets_host[-1])
+    max_seq_len, max_cands = int(max_seq_len), int(max_cands)
     if total_tokens is None:
         total_tokens = limit
     elif timestamps is not None and total_tokens > limit:
         raise ValueError("total_tokens exceeds the timestamps' length")
     with _on(q, *cache, offsets, k, v, u, cand_offsets, first_rows, timestamps, cand_timestamps,
              rab_pos, rab_time, ln_weight, ln_bias, y, workspace):
-        p = hstu_problem_t(HSTU_BF16, B, total_tokens, max_seq_len, H, 128, 128,
+        p = hstu_problem_t(HSTU_BF16, B, int(total_tokens), max_seq_len, H, 128, 128,
                            _arg(offsets, "offsets", _I32, B + 1),
                            None if offsets_host is None else offsets_host.data_ptr(),
                            _arg(timestamps, "timestamps", _I64),
                            _arg(rab_pos, "rab_pos", _F32, H, W), (W + 1) // 2,
-                           _arg(rab_time, "rab_time", _F32, H, NB), NB, norm_len, eps,
+                           _arg(rab_time, "rab_time", _F32, H, NB), NB, int(norm_len), float(eps),
                            _arg(ln_weight, "ln_weight", _F32, H * 128),
                            _arg(ln_bias, "ln_bias", _F32, H * 128))
         if rab_time is not None and timestamps is not None and total_tokens == 0:

@@ -784,7 +784,6 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
   // one grid dimension holds every (user, candidates, keys, heads) CTA, and
   // every (user, candidate); the pieces of the histories are numbered in 32 bits
   if (static_cast<double>(p->batch) * cut.cgroups * cut.splits * cut.hgroups > 2147483647.0 ||
-      static_cast<double>(p->batch) * p->max_seq_len > 1e12 ||
       (static_cast<double>(cut.ctas) + p->batch) * cut.parts * cut.hgroups > 2147483647.0 ||
       static_cast<double>(p->batch) * max_cands > 2147483647.0)
     return HSTU_ERR_UNSUPPORTED;

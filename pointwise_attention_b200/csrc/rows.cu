@@ -30,6 +30,7 @@ namespace hstu {
 namespace {
 
 constexpr int kMaxE = 16384;
+constexpr int kMaxT = 0x7FFF0000;   // a row index plus the grid's stride stays in 32 bits
 constexpr float kE4M3Max = 448.0f;
 constexpr float kAmaxFloor = 7.8886090522101181e-31f;   // 2^-100: keeps 1 / scale finite
 
@@ -540,7 +541,7 @@ HSTU_API hstu_status_t hstu_rmsnorm_fwd(hstu_dtype_t dtype, int32_t T, int32_t E
   }
   if (!aligned(weight, 4) || !aligned(q8_scale, 4) || !aligned(rstd, 4))
     return HSTU_ERR_INVALID_ARG;
-  if (E > kMaxE) return HSTU_ERR_UNSUPPORTED;
+  if (E > kMaxE || T > kMaxT) return HSTU_ERR_UNSUPPORTED;
   if (T == 0) return HSTU_OK;
   const RowsArgs a{x, residual, weight, h, y, q8, q8_scale, rstd, T, E, eps};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -556,7 +557,7 @@ HSTU_API hstu_status_t hstu_quant_rows(hstu_dtype_t dtype, int32_t T, int32_t E,
   if (st != HSTU_OK) return st;
   if (T > 0 && (!x || !q8 || !q8_scale || !aligned(x, elem_bytes(dtype)) || !aligned(q8_scale, 4)))
     return HSTU_ERR_INVALID_ARG;
-  if (E > kMaxE) return HSTU_ERR_UNSUPPORTED;
+  if (E > kMaxE || T > kMaxT) return HSTU_ERR_UNSUPPORTED;
   if (T == 0) return HSTU_OK;
   const RowsArgs a{x, nullptr, nullptr, nullptr, nullptr, q8, q8_scale, nullptr, T, E, 1.0f};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -566,7 +567,7 @@ HSTU_API hstu_status_t hstu_quant_rows(hstu_dtype_t dtype, int32_t T, int32_t E,
 }
 
 HSTU_API size_t hstu_rmsnorm_bwd_workspace_size(int32_t T, int32_t E) {
-  if (T < 0 || E < 1 || E > kMaxE) return 0;
+  if (T < 0 || T > kMaxT || E < 1 || E > kMaxE) return 0;
   const size_t n = static_cast<size_t>(bwd_blocks(T, E)) * E * sizeof(float);
   return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
@@ -585,7 +586,7 @@ HSTU_API hstu_status_t hstu_rmsnorm_bwd(hstu_dtype_t dtype, int32_t T, int32_t E
       return HSTU_ERR_INVALID_ARG;
   }
   if (!aligned(rstd, 4) || !aligned(weight, 4) || !aligned(d_weight, 4)) return HSTU_ERR_INVALID_ARG;
-  if (E > kMaxE) return HSTU_ERR_UNSUPPORTED;
+  if (E > kMaxE || T > kMaxT) return HSTU_ERR_UNSUPPORTED;
   if (d_weight && (!workspace || !aligned(workspace, 256) ||
                    workspace_bytes < hstu_rmsnorm_bwd_workspace_size(T, E)))
     return HSTU_ERR_WORKSPACE;

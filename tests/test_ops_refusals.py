@@ -44,7 +44,7 @@ RMS = dict(dt=1, T=4, E=64, p_x=FAKE, p_res=None, p_w=None, eps=1e-6, p_h=None, 
     (dict(eps=float("inf")), INV), (dict(p_q8=FAKE), INV), (dict(p_s=FAKE), INV),
     (dict(p_h=FAKE), INV), (dict(p_x=FAKE + 1), INV), (dict(p_y=FAKE + 1), INV),
     (dict(p_w=FAKE + 2), INV), (dict(p_rstd=FAKE + 2), INV), (dict(E=16385), UNS),
-    (dict(dt=0, p_x=FAKE + 2), INV)])
+    (dict(dt=0, p_x=FAKE + 2), INV), (dict(T=2 ** 31 - 1), UNS)])
 def test_rmsnorm_fwd_refusals(pa, change, want):
     assert call(pa.load_library().hstu_rmsnorm_fwd, RMS, change) == want
 
