@@ -31,7 +31,7 @@ namespace hstu {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWords = 8;   // words of a thread, kThreads apart: that many loads in flight
+constexpr int kWords = 4;   // words of a thread, kThreads apart: that many loads in flight
 
 struct Kv4Args {
   const void* src[2];    // pack: k, v bf16 [T, H, 128]; unpack: codes
@@ -75,22 +75,19 @@ __global__ void __launch_bounds__(kThreads) hstu_kv4_pack_rows(const Kv4Args a) 
   for (int j = 0; j < kWords; ++j) {
     const int64_t i = i0 + j * kThreads;
     const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-    // |x| as bit patterns: ordered like the values, NaN above infinity
-    uint32_t m = 0;
+    // |x| as bit patterns: ordered like the values, NaN above infinity; the
+    // maximum of both halves of a word at once
+    uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      m = max(m, max((w[e] << 16) & 0x7FFFFFFFu, w[e] & 0x7FFF0000u));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const float s = kv4_scale(m);
-    const float inv = 1.0f / s;
+    for (int e = 1; e < 4; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float s = kv4_scale(max(m >> 16, m & 0xFFFFu));
+    const float inv = kv4_inverse(s);
+    const uint64_t inv2 = pack_f32x2(inv, inv);
     uint32_t code = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = kv4_code(__uint_as_float(w[e] << 16) * inv);
-      const uint32_t hi = kv4_code(__uint_as_float(w[e] & 0xFFFF0000u) * inv);
-      code |= (lo << (4 * e)) | (hi << (16 + 4 * e));
-    }
+    for (int e = 0; e < 4; ++e) code |= (kv4_codes(w[e], inv2) & 0x000F000Fu) << (4 * e);
     int64_t at;
     if (i >= a.units || !cache_word(a, i, &at)) continue;
     static_cast<uint32_t*>(a.dst[which])[at] = code;

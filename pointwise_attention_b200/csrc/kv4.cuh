@@ -6,26 +6,43 @@
 
 namespace hstu {
 
-// Scale of a group whose largest |x| has the bit pattern m: the smallest
-// number of five significant bits >= max / 7, the maximum taken as at least
-// 2^-100 (so that 1 / s is finite).  A group that holds an infinity or a NaN
-// gets a NaN scale and reads as NaN.
+// Scale of a group whose largest |x| is the bf16 number with the bits m: the
+// smallest number of five significant bits >= max / 7, the maximum taken as at
+// least 2^-100 (so that 1 / s is finite).  A group that holds an infinity or a
+// NaN gets a NaN scale and reads as NaN.
+// The quotient is max times the fp32 number nearest to 1 / 7, off by less than
+// 2^-22 of itself.  Where max = 7 k for a k of five bits it has to come out at
+// or below k, and elsewhere it is 2^-9 or more away from such a k (7 k has
+// eight bits, as max has), so 64 units in the last place (2^-17) are taken off
+// before rounding upwards.
 __device__ __forceinline__ float kv4_scale(uint32_t m) {
-  if (m >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  const float top = fmaxf(__uint_as_float(m), 7.8886090522101181e-31f);
-  const uint32_t s = __float_as_uint(__fdiv_rn(top, 7.0f));
-  return __uint_as_float((s + 0x7FFFFu) & ~0x7FFFFu);
+  if (m >= 0x7F80u) return __uint_as_float(0x7FC00000u);
+  const float top = fmaxf(__uint_as_float(m << 16), 7.8886090522101181e-31f);
+  const uint32_t s = __float_as_uint(top * 0.14285714924335479736f);
+  return __uint_as_float((s - 64u + 0x7FFFFu) & ~0x7FFFFu);
 }
 
-// rint(x / s) + 8 for q = x * (1 / s) in fp32.  q carries a relative error of
-// 2^-23; exact quotients of an 8-bit by a 5-bit significand are either ties
-// or 2^-10 and more away from one, so rounding q to a multiple of 2^-11 first
-// (adding and taking away 1.5 * 2^12) restores ties, and the second rounding
-// sends them to even as the exact quotient's would.
-__device__ __forceinline__ uint32_t kv4_code(float q) {
-  const float t = __fadd_rn(__fadd_rn(q, 6144.0f), -6144.0f);
-  // 1.5 * 2^23 + 8: the low bits of the sum are the whole number plus 8
-  return __float_as_uint(__fadd_rn(t, 12582920.0f)) & 15u;
+// 1 / s to one unit in the last place.
+__device__ __forceinline__ float kv4_inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// The codes n + 8 of a bf16 pair w, in bits 0..3 and 16..19 (the other bits
+// hold anything): n = rint(x / s) for q = x (1 / s) in fp32, which is off by
+// less than 2^-22 of itself.  Exact quotients of an 8-bit by a 5-bit
+// significand are either ties or 2^-10 and more away from one, so rounding q to
+// a multiple of 2^-11 first (adding and taking away 1.5 * 2^12) restores ties,
+// and the second rounding sends them to even as the exact quotient's would.
+// The last constant is 1.5 * 2^23 + 8: the low bits of the sum are n + 8.
+__device__ __forceinline__ uint32_t kv4_codes(uint32_t w, uint64_t inv2) {
+  uint64_t q = fmul2(pack_f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), inv2);
+  q = fadd2(q, pack_f32x2(6144.0f, 6144.0f));
+  q = fadd2(q, pack_f32x2(-6144.0f, -6144.0f));
+  q = fadd2(q, pack_f32x2(12582920.0f, 12582920.0f));
+  const float2 f = unpack_f32x2(q);
+  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x5410);
 }
 
 // bf16 pair (value 2I, value 2I + 1) of a word of eight: 128 + (n + 8) is the

@@ -66,6 +66,19 @@ def test_pack_and_unpack(T, H):
         assert bool((err <= top / 7 * 17 / 32).all())
 
 
+def test_every_maximum():
+    """Groups whose largest magnitude runs through all 32640 finite bf16
+    numbers: scales and codes are the definition's, ties among them."""
+    bits = torch.arange(0x7F80, dtype=torch.int32).to(torch.int16)
+    top = bits.view(BF16).to(DEV).view(4080, 2, 4, 1)
+    f = torch.cat([torch.tensor([1.0, -0.5, 0.25, -0.125]), 2 * torch.rand(28, generator=gen(1)) - 1])
+    x = (top.double() * f.double().to(DEV)).to(BF16).flatten(2)
+    cache = pa.hstu_kv4_pack(x, -x)
+    n, s = groups64(x)
+    assert torch.equal(cache[1].double(), s) and torch.equal(cache[3].double(), s)
+    assert torch.equal(cache[0], codes64(n)) and torch.equal(cache[2], codes64(-n))
+
+
 def test_rows_holes_and_bad_rows():
     R, H = 50, 4
     cache = pa.hstu_kv4_cache(R, H, DEV)
