@@ -572,7 +572,10 @@ def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: 
         _on(x8, *outs)
     with _on(x8, x_scale, w8, w_scale, bias, workspace):
         if out is None:
-            u, v, q, k = (x8.new_empty(sh, dtype=_BF16) for sh in shapes)
+            u = x8.new_empty(shapes[0], dtype=_BF16)
+            v = x8.new_empty(shapes[1], dtype=_BF16)
+            q = torch.empty_like(v) if d_qk == d_v else x8.new_empty(shapes[2], dtype=_BF16)
+            k = torch.empty_like(q)
             out = dict(u=u, v=v, q=q, k=k)
             ptrs = u.data_ptr(), v.data_ptr(), q.data_ptr(), k.data_ptr()
         workspace, wp, wn = _room(workspace, x8)

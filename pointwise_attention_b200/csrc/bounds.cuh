@@ -22,8 +22,7 @@ enum BoundsSite {
   BS_FWD_TS = 1, BS_FWD_TMA_Q, BS_FWD_TMA_KV, BS_FWD_ROW,
   BS_BWD_TS = 10, BS_BWD_TMA_Q, BS_BWD_TMA_K, BS_BWD_ROW,
   BS_CAND_TS = 20, BS_CAND_TMA, BS_CAND_ROW, BS_CAND_CNT,
-  BS_PROJ_TMA = 30, BS_SIMT_TS = 40,
-  BS_CAND4_TS = 50, BS_CAND4_ROW, BS_CAND4_KEY
+  BS_PROJ_TMA = 30, BS_SIMT_TS = 40
 };
 
 static __device__ __noinline__ void report_bounds(int* status, int site, long long idx) {

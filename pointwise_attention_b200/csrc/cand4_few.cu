@@ -31,14 +31,22 @@
 // The pieces' sums go to the workspace in fp32; a second kernel adds them in
 // order (the result does not depend on timing), adds the self term and applies
 // the LayerNorm and the gate.
+//
+// Measured on a B200: one candidate for each of 32 users, 8 heads, histories of
+// 256-4096 tokens (81 MB of cache): 46 us (the bytes alone take 12).  Issue
+// slots bound it, half busy with 16 warps an SM: some 500 instructions per 16
+// keys and head, of which decoding takes 200, with 19 us of starts and the last
+// kernel (a user's 16 keys).  A CTA per (user, run of keys) left SMs idle at the
+// end (64 us); cp.async by the lanes cost 145 shared-memory wavefronts a block.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <atomic>
 
 #include "bounds.cuh"
-#include "internal.h"
+#include "internal_ops.h"
 #include "kv4.cuh"
+#include "ops.cuh"
 #include "ptx.cuh"
 #include "tile_math.cuh"
 
@@ -760,7 +768,9 @@ cudaError_t launch_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t str
 
 }  // namespace
 
-// More candidates per user than this take the tcgen05 kernel.
+// More candidates per user than this take the tcgen05 kernel: for 32 users, 8
+// heads and 2176 keys, up to 7 candidates take 43 us and up to 15 take 70 us
+// here, and up to 23 take 150 us there, as much as two passes here would.
 constexpr int kFewMax = 16;
 
 Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands, int total_tokens) {

@@ -13,6 +13,7 @@
 
 #include "hstu.h"
 #include "internal.h"
+#include "internal_ops.h"
 
 using namespace hstu;
 

@@ -156,27 +156,6 @@ struct ProjArgs {
   float eps;
 };
 
-// Arguments of the UVQK projection of 8-bit rows.
-struct Proj8Args {
-  const float* x_scale;     // [T]
-  const float* w_scale;     // [N]
-  const float* bias;        // [N] or nullptr
-  void* out0;               // u [T, Nu]
-  void* out1;               // v [T, Nu]
-  void* out2;               // q [T, Nq]
-  void* out3;               // k [T, Nq]
-  int* status;
-  int T, E, Nu, Nq;
-  int act;                  // 1 = SiLU after the bias
-  int vec32;                // every output pointer is 32-byte aligned
-};
-
-// The outputs u, v, q, k as [T, columns] bf16, boxes of 32 columns x 32 rows
-// with the 64-byte swizzle.
-struct Proj8Outs {
-  CUtensorMap map[4];
-};
-
 // Arguments of the candidate-scoring kernel (scoring against cached histories).
 struct CandArgs {
   const int32_t* offsets;        // history [B+1]
@@ -210,58 +189,6 @@ struct CandArgs {
   BucketTable bt;
 };
 
-// Arguments of candidate scoring against histories in a 4-bit cache (kv4.cu
-// has the cache's layout).
-struct Cand4Args {
-  const int32_t* offsets;        // history [B+1]
-  const int32_t* cand_offsets;   // candidates [B+1]
-  const int32_t* first_rows;     // [B] cache row of each history's first token, or nullptr: offsets
-  const int64_t* timestamps;     // history [T] (with a time table)
-  const int64_t* cand_ts;        // candidates [C] (with a time table)
-  const float* rab_pos;          // [H, 2L-1] or nullptr
-  const float* rab_time;         // [H, nb] or nullptr
-  const uint8_t* k_codes;        // cache [R, H, 64]
-  const uint16_t* k_scales;      // cache [R, H, 4] bf16
-  const uint8_t* v_codes;
-  const uint16_t* v_scales;
-  const void* q;                 // candidates [C, H, 128] bf16
-  const void* k;
-  const void* v;
-  const void* u;                 // candidates [C, H*128]
-  void* y;                       // candidates [C, H*128]
-  const float* ln_weight;        // [H*128] or nullptr
-  const float* ln_bias;
-  // workspace: sums over the history, [slices][C][H*128] fp32; a slice is the
-  // part of a history that one warp (many candidates: one CTA) walks
-  float* part;
-  const uint32_t* plan;          // many candidates, with a time table: CandArgs::plan
-  int* status;
-  int B, T, C, H, R;
-  int max_seq_len, max_cands;
-  int L, nb, norm_len;
-  int chunk, splits;             // history keys per CTA, CTAs along the longest history
-  float eps;
-  BucketTable bt;
-};
-
-// How a problem is cut (sizes alone decide).
-struct Cand4Cut {
-  int many;      // the kernel for many candidates: 256 of them, a head a CTA
-  int heads;     // few: heads of a CTA, one warp each, times
-  int parts;     // few: warps that share a head's keys (many: 1)
-  int hgroups;   // CTAs along the heads
-  int nt;        // few: groups of 8 candidates of a CTA
-  int ctas;      // few: shares of the tokens
-  int cgroups;   // many: CTAs along a user's candidates
-  int chunk, splits;   // many: history keys per CTA, CTAs along the longest history
-};
-Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands, int total_tokens);
-// Rows (of H*128 fp32) that hold the sums of every cut with H heads, at most B
-// histories of max_seq_len and at most C candidates, max_cands a user, and the
-// bytes of the many-candidate kernel's time plans: both grow with each of them.
-size_t cand4_part_rows(int B, int H, int max_seq_len, int C, int max_cands);
-size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands);
-
 // The synchronous argument checks of hstu_attn_bwd (all but the workspace's).
 hstu_status_t check_bwd_args(const hstu_problem_t* p, const void* dy, const void* q,
                              const void* k, const void* v, const void* u, const float* o_save,
@@ -279,15 +206,8 @@ cudaError_t launch_bwd_bf16_simt(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd_pre_bf16(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_cand_sm100(const CandArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);
-cudaError_t launch_cand4_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t stream);
-cudaError_t launch_cand4_sm100(const Cand4Args& a, const CUtensorMap& tq, cudaStream_t stream);
-cudaError_t launch_cand4_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_sums,
-                                cudaStream_t stream);
 cudaError_t launch_uvqk_sm100(const ProjArgs& a, const CUtensorMap& tx, const CUtensorMap& tw,
                               cudaStream_t stream);
-int uvqk_fp8_cols(int T, int E, int N);   // columns of a tile of the 8-bit projection
-cudaError_t launch_uvqk_fp8_sm100(const Proj8Args& a, const CUtensorMap& tx, const CUtensorMap& tw,
-                                  const Proj8Outs& to, cudaStream_t stream);
 cudaError_t launch_out_sm100(const ProjArgs& a, const CUtensorMap& ty, const CUtensorMap& tw,
                              cudaStream_t stream);
 cudaError_t launch_time_plans(const PlanArgs& a, cudaStream_t stream);

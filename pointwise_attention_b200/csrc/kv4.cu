@@ -17,7 +17,9 @@
 // Scales [rows, H, 4] bf16.
 //
 // Both directions move 2 * 256 B of bf16 and 2 * 72 B of cache per token and
-// head, once: HBM bounds them.
+// head, once: HBM bounds them.  Measured on a B200, 69637 tokens of 8 heads (365
+// MB each way): 168 us for both, 4.4 TB/s (one word a thread, divisions and
+// one-element arithmetic: 407 us).
 #include <cuda_bf16.h>
 #include <nvtx3/nvToolsExt.h>
 

@@ -2,6 +2,7 @@
 #pragma once
 #include <cstdint>
 
+#include "ops.cuh"
 #include "tile_math.cuh"
 
 namespace hstu {

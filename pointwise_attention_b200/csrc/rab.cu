@@ -11,6 +11,10 @@
 // forward looks a quad's first bucket up by bisection and steps from there,
 // the backward is a sum over ranges.  Both move 4 bytes per table entry and
 // are bound by the launch up to some hundred thousand entries, then by HBM.
+// Measured on a B200: table of 8 heads x 16383 entries from 32 buckets 6 us;
+// gradient of 32 heads x 100003 distances 9 us (12.8 MB; half of it is the
+// cluster's start, its barriers and the tables; walking runs of distances and
+// segmenting at the borders took 17 us).
 #include <cooperative_groups.h>
 #include <nvtx3/nvToolsExt.h>
 

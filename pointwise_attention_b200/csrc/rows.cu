@@ -15,6 +15,12 @@
 // Sums, statistics and products are fp32.  h is rounded to the stream's type
 // before the norm because that is the value which the next layer and the
 // backward read; y and q8 take v unrounded.
+//
+// Measured on a B200 (copies reach 6.56 TB/s): 131071 x 512 bf16 with a residual
+// to h, 8 bits, scales and rstd, 471 MB: 84 us (5.6 TB/s; 128 us with one-element
+// arithmetic, whose 470 instructions a row were what bounded it); backward of
+// 32768 x 512 bf16 with d_residual, 134 MB: 39 us and 6 us for the weight's sums
+// (3.4 TB/s: nine rows a warp, latency bounds it).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <nvtx3/nvToolsExt.h>
@@ -24,6 +30,7 @@
 
 #include "hstu.h"
 #include "internal.h"
+#include "ops.cuh"
 #include "tile_math.cuh"
 
 namespace hstu {
