@@ -25,6 +25,7 @@
 #include <cuda_fp8.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -187,6 +188,52 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// Rows on their way from HBM: where a warp owns a row and takes it in 16-byte
+// vectors, it copies the rows that it will come to asynchronously to shared
+// memory, kDepth - 1 rows ahead.  Every lane copies what it reads itself, so its
+// own wait for its copies is all that stands between the two.
+template <typename T, int VEC, int TPR, int NV, int TENSORS>
+struct Ring {
+  static constexpr bool on = VEC > 1 && TPR == 32;
+  static constexpr int kDepth = NV <= 4 ? 3 : 2;
+  static constexpr int kBytes = on ? 8 * kDepth * TENSORS * NV * 512 : 0;   // 8 rows a block
+  uint4* mine;   // of this lane: [stage][tensor][vector], 32 vectors apart
+  int lane, E, stage;
+
+  __device__ __forceinline__ Ring(void* smem, int sub, int lane_, int E_)
+      : mine(static_cast<uint4*>(smem) + (sub * kDepth * TENSORS * NV) * 32 + lane_),
+        lane(lane_), E(E_), stage(0) {}
+  __device__ __forceinline__ uint4* slot(int st, int tensor, int i) const {
+    return mine + ((st * TENSORS + tensor) * NV + i) * 32;
+  }
+  __device__ __forceinline__ void copy(int st, int tensor, const T* row) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * VEC;
+      if (c < E)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(
+                         __cvta_generic_to_shared(slot(st, tensor, i)))),
+                     "l"(row + c)
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ static void wait() {   // all but the newest kDepth - 2 groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+  }
+  __device__ __forceinline__ void read(int tensor, Pack<T, VEC> (&p)[NV]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if ((i * TPR + lane) * VEC < E) {
+        *reinterpret_cast<uint4*>(&p[i]) = *slot(stage, tensor, i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p[i].v[e] = Elem<T>::put(0.f);
+      }
+    }
+  }
+};
+
 // NORM: the norm; otherwise the rows as they are (quantisation alone).
 template <typename T, int VEC, int TPR, int NV, bool NORM>
 __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / block_threads<TPR>() : 1)
@@ -302,7 +349,9 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
   constexpr int kRows = block_threads<TPR>() / TPR;
   constexpr int N = NV * VEC, P = N / 2;
   __shared__ float red[TPR > 32 ? TPR / 32 : 1];
-  __shared__ float sdw[TPR == 32 ? kRows : 1][TPR == 32 ? 32 * N : 1];
+  // the rows' ring and, after the rows, the warps' weight sums [kRows][32 N]
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  using R = Ring<T, VEC, TPR, NV, 3>;
   const int lane = TPR == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int sub = TPR == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -319,18 +368,41 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
   const int stride = static_cast<int>(gridDim.x) * kRows;
   int t = static_cast<int>(blockIdx.x) * kRows + sub;
   Pack<T, VEC> pd[NV], ph[NV], pr[NV];
-  float rn = 0.f;
-  auto load = [&](int row) {
-    const size_t at = static_cast<size_t>(row) * a.E;
-    load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.dy) + at, lane, a.E, pd);
-    load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.h) + at, lane, a.E, ph);
-    rn = __ldg(a.rstd + row);
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* h = static_cast<const T*>(a.h);
+  const T* dres = static_cast<const T*>(a.dres);
+  R ring(s_dyn, sub, lane, a.E);
+  auto send = [&](int row, int st) {   // rows past T are not copied; their group is empty
+    if (row < a.T) {
+      const size_t at = static_cast<size_t>(row) * a.E;
+      ring.copy(st, 0, dy + at);
+      ring.copy(st, 1, h + at);
+      if (dres) ring.copy(st, 2, dres + at);
+    }
+    R::commit();
   };
+  float rn = t < a.T ? __ldg(a.rstd + t) : 0.f;
+  if constexpr (R::on) {
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i) send(t + i * stride, i);
+  }
   for (; t < a.T; t += stride) {
     const size_t at = static_cast<size_t>(t) * a.E;
-    load(t);
-    if (a.dres) load_row<T, VEC, TPR, NV>(static_cast<const T*>(a.dres) + at, lane, a.E, pr);
+    if constexpr (R::on) {
+      R::wait();
+      ring.read(0, pd);
+      ring.read(1, ph);
+      if (dres) ring.read(2, pr);
+      // the stage of the row before is free
+      send(t + (R::kDepth - 1) * stride, ring.stage == 0 ? R::kDepth - 1 : ring.stage - 1);
+      ring.stage = ring.stage == R::kDepth - 1 ? 0 : ring.stage + 1;
+    } else {
+      load_row<T, VEC, TPR, NV>(dy + at, lane, a.E, pd);
+      load_row<T, VEC, TPR, NV>(h + at, lane, a.E, ph);
+      if (dres) load_row<T, VEC, TPR, NV>(dres + at, lane, a.E, pr);
+    }
     const float r = rn;
+    if (t < a.T - stride) rn = __ldg(a.rstd + t + stride);
     const uint64_t r2 = pack_f32x2(r, r);
     // g = w dy and z = h r: dx = r g - z (r mean(g z)), dw += dy z; g and z are
     // made twice, which leaves registers for more rows on an SM
@@ -352,7 +424,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
       const uint64_t g = fmul2(get_pair<T, VEC, NV>(pd, i), w[i]);
       const uint64_t z = fmul2(get_pair<T, VEC, NV>(ph, i), r2);
       uint64_t x = ffma2(z, k2, fmul2(g, r2));
-      if (a.dres) x = fadd2(x, get_pair<T, VEC, NV>(pr, i));
+      if (dres) x = fadd2(x, get_pair<T, VEC, NV>(pr, i));
       put_pair<T, VEC, NV>(pd, i, x);
     }
 #pragma unroll
@@ -371,14 +443,17 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
   if (!a.partial) return;
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * a.E;
   if (TPR == 32) {
-    // the warps' sums of the block, added in warp order
+    // the warps' sums of the block, added in warp order, over the ring's room
+    float* sdw = reinterpret_cast<float*>(s_dyn);
+    if constexpr (R::on) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) sdw[sub][(i / VEC * 32 + lane) * VEC + i % VEC] = dw[i];
+    for (int i = 0; i < N; ++i) sdw[sub * 32 * N + (i / VEC * 32 + lane) * VEC + i % VEC] = dw[i];
     __syncthreads();
     for (int c = static_cast<int>(threadIdx.x); c < a.E; c += block_threads<TPR>()) {
       float s = 0.f;
 #pragma unroll
-      for (int g = 0; g < kRows; ++g) s += sdw[g][c];
+      for (int g = 0; g < kRows; ++g) s += sdw[g * 32 * N + c];
       part[c] = s;
     }
   } else {
@@ -390,30 +465,31 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
   }
 }
 
-// dw[c] = the blocks' partial sums added in a fixed order: 32 columns by 32
-// block strides per CTA.
+// dw[c] = the blocks' partial sums added in a fixed order: 8 columns by 128
+// strides of blocks per CTA, four loads in flight a thread.
 __global__ void __launch_bounds__(1024) hstu_rows_dw(const float* partial, int blocks, int E,
                                                      float* dw) {
-  __shared__ float red[32][33];
-  const int cx = static_cast<int>(threadIdx.x & 31), gy = static_cast<int>(threadIdx.x >> 5);
-  const int c = static_cast<int>(blockIdx.x) * 32 + cx;
+  __shared__ float red[8][129];
+  const int cx = static_cast<int>(threadIdx.x & 7), gy = static_cast<int>(threadIdx.x >> 3);
+  const int c = static_cast<int>(blockIdx.x) * 8 + cx;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the rows' kernel runs
   float s = 0.f;
-  if (c < E) {
-    // eight loads in flight, added in order
-    for (int g = gy; g < blocks; g += 256) {
-      float v[8];
+  if (c < E)
+    for (int g = gy; g < blocks; g += 4 * 128) {
+      float v[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = g + 32 * i < blocks ? partial[static_cast<size_t>(g + 32 * i) * E + c] : 0.f;
+      for (int i = 0; i < 4; ++i)
+        v[i] = g + 128 * i < blocks ? partial[static_cast<size_t>(g + 128 * i) * E + c] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i];
+      for (int i = 0; i < 4; ++i) s += v[i];
     }
-  }
-  red[gy][cx] = s;
+  red[cx][gy] = s;
   __syncthreads();
-  s = warp_sum(red[cx][gy]);   // column gy of the tile
-  if (cx == 0 && static_cast<int>(blockIdx.x) * 32 + gy < E) dw[blockIdx.x * 32 + gy] = s;
+  const int col = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  if (col >= 8) return;
+  s = (red[col][lane] + red[col][lane + 32]) + (red[col][lane + 64] + red[col][lane + 96]);
+  s = warp_sum(s);
+  if (lane == 0 && static_cast<int>(blockIdx.x) * 8 + col < E) dw[blockIdx.x * 8 + col] = s;
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -459,6 +535,23 @@ cudaError_t pick_shape(bool vec, int E, F&& f) {
   return f(Shape<1, 512, 32>{});
 }
 
+// Opts a kernel in to its shared memory, once per device and kernel (S, T and
+// KIND tell the kernels apart).
+template <typename S, typename T, int KIND, typename K>
+cudaError_t opt_in(K kernel, int smem) {
+  if (smem <= 48 * 1024) return cudaSuccess;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  return cudaSuccess;
+}
+
 template <typename T, bool NORM>
 cudaError_t launch_rows_fwd(const RowsArgs& a, cudaStream_t stream) {
   constexpr size_t V = 16;
@@ -495,12 +588,18 @@ cudaError_t launch_rows_bwd(const RowsBwdArgs& a, float* dw, cudaStream_t stream
   const int blocks = bwd_blocks(a.T, a.E);
   const cudaError_t err = pick_shape<T>(vec, a.E, [&](auto s) {
     using S = decltype(s);
-    hstu_rows_bwd<T, S::VEC, S::TPR, S::NV><<<blocks, block_threads<S::TPR>(), 0, stream>>>(a);
+    using R = Ring<T, S::VEC, S::TPR, S::NV, 3>;
+    constexpr int sums = S::TPR == 32 ? 8 * 32 * S::NV * S::VEC * 4 : 0;
+    constexpr int smem = R::kBytes > sums ? R::kBytes : sums;
+    auto kernel = hstu_rows_bwd<T, S::VEC, S::TPR, S::NV>;
+    const cudaError_t e = opt_in<S, T, 0>(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, block_threads<S::TPR>(), smem, stream>>>(a);
     return cudaGetLastError();
   });
   if (err != cudaSuccess || !dw) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.E + 31) / 32));
+  cfg.gridDim = dim3(static_cast<unsigned>((a.E + 7) / 8));
   cfg.blockDim = dim3(1024);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
