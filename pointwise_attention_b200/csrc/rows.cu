@@ -17,10 +17,11 @@
 // backward read; y and q8 take v unrounded.
 //
 // Measured on a B200 (copies reach 6.56 TB/s): 131071 x 512 bf16 with a residual
-// to h, 8 bits, scales and rstd, 471 MB: 84 us (5.6 TB/s; 128 us with one-element
-// arithmetic, whose 470 instructions a row were what bounded it); backward of
-// 32768 x 512 bf16 with d_residual, 134 MB: 39 us and 6 us for the weight's sums
-// (3.4 TB/s: nine rows a warp, latency bounds it).
+// to h, 8 bits, scales and rstd, 471 MB: 80 us (5.9 TB/s; 90 us with the next
+// row's loads in registers, 128 us with one-element arithmetic, whose 470
+// instructions a row were what bounded it); backward of 32768 x 512 bf16 with
+// d_residual, 134 MB: 37 us with the kernel of the weight's sums (3.6 TB/s: nine
+// rows a warp; 45 us without the ring).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <nvtx3/nvToolsExt.h>
@@ -253,8 +254,8 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
     for (int i = 0; i < P; ++i) w[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
   }
   // The loop is uniform over the threads of a row, and over the block where
-  // the block is the row.  The next row's loads are issued before this row's
-  // sums are waited for.
+  // the block is the row.  Without the ring the next row's loads are issued
+  // before this row's sums are waited for.
   const int stride = static_cast<int>(gridDim.x) * kRows;
   int t = static_cast<int>(blockIdx.x) * kRows + sub;
   Pack<T, VEC> p[NV], q[NV];
@@ -262,9 +263,32 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
     load_row<T, VEC, TPR, NV>(x + static_cast<size_t>(row) * a.E, lane, a.E, p);
     if (NORM && res) load_row<T, VEC, TPR, NV>(res + static_cast<size_t>(row) * a.E, lane, a.E, q);
   };
-  if (t < a.T) load(t);
+  using R = Ring<T, VEC, TPR, NV, 2>;
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  R ring(s_dyn, sub, lane, a.E);
+  auto send = [&](int row, int st) {   // rows past T are not copied; their group is empty
+    if (row < a.T) {
+      ring.copy(st, 0, x + static_cast<size_t>(row) * a.E);
+      if (NORM && res) ring.copy(st, 1, res + static_cast<size_t>(row) * a.E);
+    }
+    R::commit();
+  };
+  if constexpr (R::on) {
+#pragma unroll
+    for (int i = 0; i < R::kDepth - 1; ++i) send(t + i * stride, i);
+  } else {
+    if (t < a.T) load(t);
+  }
   for (; t < a.T; t += stride) {
     const size_t at = static_cast<size_t>(t) * a.E;
+    if constexpr (R::on) {
+      R::wait();
+      ring.read(0, p);
+      if (NORM && res) ring.read(1, q);
+      // the stage of the row before is free
+      send(t + (R::kDepth - 1) * stride, ring.stage == 0 ? R::kDepth - 1 : ring.stage - 1);
+      ring.stage = ring.stage == R::kDepth - 1 ? 0 : ring.stage + 1;
+    }
     if (NORM && res) {
 #pragma unroll
       for (int i = 0; i < P; ++i)
@@ -281,7 +305,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
     uint64_t v[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = get_pair<T, VEC, NV>(p, i);
-    if (t < a.T - stride) load(t + stride);
+    if (!R::on && t < a.T - stride) load(t + stride);
     if (NORM) {
       uint64_t ss2 = 0ull;
 #pragma unroll
@@ -564,8 +588,11 @@ cudaError_t launch_rows_fwd(const RowsArgs& a, cudaStream_t stream) {
     // eight blocks per SM at most: each row's loads then run ahead of it
     const int64_t need = (static_cast<int64_t>(a.T) + kRows - 1) / kRows;
     const int blocks = static_cast<int>(need < 8 * 148 ? need : 8 * 148);
-    hstu_rows_fwd<T, S::VEC, S::TPR, S::NV, NORM>
-        <<<blocks, block_threads<S::TPR>(), 0, stream>>>(a);
+    constexpr int smem = Ring<T, S::VEC, S::TPR, S::NV, 2>::kBytes;
+    auto kernel = hstu_rows_fwd<T, S::VEC, S::TPR, S::NV, NORM>;
+    const cudaError_t err = opt_in<S, T, NORM ? 1 : 2>(kernel, smem);
+    if (err != cudaSuccess) return err;
+    kernel<<<blocks, block_threads<S::TPR>(), smem, stream>>>(a);
     return cudaGetLastError();
   });
 }

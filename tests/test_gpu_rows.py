@@ -143,6 +143,29 @@ def test_norm_backward_many_rows_repeats_bitwise():
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("dtype,E", [(BF16, 24), (F32, 20), (BF16, 520), (F32, 7)])
+def test_many_rows_a_warp(dtype, E):
+    """Every warp walks several rows (more than are under way at a time)."""
+    T = 50021 if E < 500 else 30011
+    x, res, dy = (rows(s, T, E, dtype) for s in (1, 2, 3))
+    rel = (E + 16) * U
+    h, rstd, v = norm64(x, res, None, dtype)
+    out = pa.hstu_rmsnorm_fwd(x, residual=res, eps=EPS, save_rstd=True)
+    assert torch.equal(out["h"], h)
+    within(out["rstd"], rstd, rel * rstd, "rstd")
+    within(out["y"], v, v.abs() * (HALF[dtype] + 2 * rel), "y")
+    q8, s = pa.hstu_quant_rows(x)
+    check_q8(q8, s, x.double(), E, "q8")
+    dx, dw = pa.hstu_rmsnorm_bwd(dy, h, out["rstd"], d_residual=res)
+    hd, dyd, r = h.double(), dy.double(), out["rstd"].double()[:, None]
+    m, mabs = (dyd * hd).mean(1, keepdim=True), (dyd * hd).abs().mean(1, keepdim=True)
+    ref = r * (dyd - hd * r * r * m) + res.double()
+    tol = r * (dyd.abs() * 4 * U + hd.abs() * r * r * mabs * rel) + res.double().abs() * 2 * U
+    within(dx, ref, tol + ref.abs() * (HALF[dtype] + 2 * U), "dx")
+    terms = dyd * hd * r
+    within(dw, terms.sum(0), terms.abs().sum(0) * (T + 8) * U, "dw")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T,E", SHAPES)
 def test_quant_rows(T, E, dtype):
