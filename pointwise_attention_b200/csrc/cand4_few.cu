@@ -814,7 +814,11 @@ size_t cand4_part_rows(int B, int H, int max_seq_len, int C, int max_cands) {
 }
 
 size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands) {
-  return max_cands > kFewMax ? (static_cast<size_t>(max_seq_len) + 127) / 128 * 16 * C : 0;
+  return max_cands > kFewMax ? cand4_near_offset(max_seq_len, C) + static_cast<size_t>(C) * 32 * kCand4Near : 0;
+}
+
+size_t cand4_near_offset(int max_seq_len, int C) {
+  return ((static_cast<size_t>(max_seq_len) + 31) / 32 * 4 * C + 255) / 256 * 256;
 }
 
 cudaError_t launch_cand4_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_sums,

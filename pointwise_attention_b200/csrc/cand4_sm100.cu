@@ -27,8 +27,8 @@
 // status word and the CTA leaves through the same barriers.
 //
 // Measured on a B200: 512 candidates for each of 32 users, 8 heads, histories of
-// 256-4096 tokens, position and time bias, 146 GFLOP: 312 us here, 385 us with the
-// plan pass (17) and the last kernel (61).  Latency bounds it: a key tile's chain of products, epilogue and
+// 256-4096 tokens, position and time bias, 146 GFLOP: 311 us here, 380 us with the
+// plan pass (15) and the last kernel (59).  Latency bounds it: a key tile's chain of products, epilogue and
 // barriers takes about 5300 cycles where the tensor core needs 2200 and tanh
 // 2048.  Half tiles with barriers of their own (64 keys) did not help: their
 // MMAs take as long to issue as whole ones.
@@ -112,7 +112,7 @@ __device__ __forceinline__ bool flagged(bool ok, int* status) {
 
 // P pairs of one 32-key block from its scores: h = S / 2 + half bias, h + h tanh h.
 // tv, ts: the plan's half biases and split columns (tile_math.cuh).
-template <bool POS, int TB>
+template <bool POS, int TB>   // (TB_BYTES: ts32 are the scores' bucket bytes)
 __device__ __forceinline__ void p_block(const uint32_t (&sv)[32], const float* pos,
                                         const uint32_t* ts32, const float (&tv)[4], const int (&ts)[3],
                                         uint32_t my32, const Tab& tab, uint32_t (&packed)[16]) {
@@ -127,13 +127,14 @@ __device__ __forceinline__ void p_block(const uint32_t (&sv)[32], const float* p
     } else {
       h2 = ffma2(s2, half2, TB == TB_CONST ? tc2 : 0ull);
     }
-    if (TB == TB_SPLIT || TB == TB_MULTI || TB == TB_GEN32) {
+    if (TB == TB_SPLIT || TB == TB_MULTI || TB == TB_GEN32 || TB == TB_BYTES) {
       float b[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int c = 2 * i + e;
         if (TB == TB_SPLIT) b[e] = c < ts[0] ? tv[0] : tv[1];
         if (TB == TB_MULTI) b[e] = c >= ts[2] ? tv[3] : c >= ts[1] ? tv[2] : c >= ts[0] ? tv[1] : tv[0];
+        if (TB == TB_BYTES) b[e] = tab.rabt()[(ts32[c >> 2] >> (8 * (c & 3))) & 0x7Fu];
         if (TB == TB_GEN32) {
           const int d = static_cast<int>(ts32[c] - my32);
           b[e] = tab.rabt()[bucket32(static_cast<uint32_t>(d < 0 ? -d : d), tab.oct())];
@@ -457,11 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t saddr = lane_addr + 128u * g;
     const size_t D = static_cast<size_t>(a.H) * 128;
     bool ok = true;
+    bool round_first = true;
     unsigned tn = 0, done = 0, en = 0;   // tiles and items so far, this candidate tile's S
     for (unsigned round = 0; round < rounds; ++round) {
       // (what the tiles need of the item; the rest is looked up again, so that
       // it holds no registers meanwhile)
-      int keys, nt, cand, rows, tiles;
+      int keys, nt, cand, rows, tiles, near0;
       const uint32_t* plan = nullptr;
       {
         Item it;
@@ -473,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rows past the last candidate repeat it, so that a warp's plans are of one kind
         cand = it.cand0 + min(r, it.rows - 1);
         if (TIME) plan = a.plan + static_cast<size_t>(it.key0 / 32) * a.C + cand;
+        near0 = (it.nb - it.key0 + 31) / 32 - 1;   // blocks from the item's first to the history's last
         tab.rabh_ = reinterpret_cast<const float*>(smem + kOffRabH) + it.h * kMaxBuckets;
       }
       const bool live = 128 * g + 32 * q4 < rows;    // the warp has candidates
@@ -486,6 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (128 * n + 32 * i < keys) pw[i] = __ldg(plan + static_cast<size_t>(i) * a.C);
         plan += static_cast<size_t>(4) * a.C;
       };
+      if (TIME && round_first) {
+        // the plan pass, which this kernel is launched beside, is over
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        round_first = false;
+      }
       if (TIME && live) load_plans(0);
       for (int n = 0; n < nt && g < tiles; ++n) {
         const unsigned slot = (tn + n) & (kRing - 1);
@@ -532,6 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tv[2] = tab.rabt()[max(tp.k_a - 2, 0)];
                 tv[3] = tab.rabt()[max(tp.k_a - 3, 0)];
                 p_block<POS, TB_MULTI>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
+              } else if (tb == TB_GEN32 && near0 - (4 * n + cc) < kCand4Near) {
+                const uint4* src = a.near + (static_cast<size_t>(near0 - (4 * n + cc)) * a.C + cand) * 2;
+                const uint4 lo = __ldg(src), hi = __ldg(src + 1);
+                const uint32_t bytes[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                p_block<POS, TB_BYTES>(sv, pos, bytes, tv, tp.s, my32, tab, packed);
               } else if (tb == TB_GEN32) {
                 p_block<POS, TB_GEN32>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
               } else {
@@ -603,6 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) *abort_flag = 1;
     tc_fence_before();
   }
+  // (also where a CTA had nothing to score: this kernel ends after the plan pass)
+  if (TIME) asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -626,8 +641,19 @@ cudaError_t launch_t(const Cand4Args& a, const CUtensorMap& tq, cudaStream_t str
                          static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.H) *
                          static_cast<unsigned>(a.B);
   const unsigned grid = items < 148u ? items : 148u;
-  hstu_cand4_sm100<POS, TIME><<<grid, kThreads, kSmem, stream>>>(tq, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  // with a time table: beside the plan pass, which the epilogue waits for (what
+  // else is read was there before the plan pass began)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = TIME ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, hstu_cand4_sm100<POS, TIME>, tq, a);
 }
 
 cudaError_t launch_cand4_sm100(const Cand4Args& a, const CUtensorMap& tq, cudaStream_t stream) {

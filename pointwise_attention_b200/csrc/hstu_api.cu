@@ -835,28 +835,12 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
     CUtensorMap tq;
     if (!make_map_3d(&tq, q, total_cands, p->num_heads, 128)) return HSTU_ERR_CUDA;
     if (p->rab_time) {
-      uint32_t* plan = reinterpret_cast<uint32_t*>(
-          static_cast<uint8_t*>(workspace) + kStatusBytes +
-          align_up(cand4_part_rows(p->batch, p->num_heads, p->max_seq_len, total_cands, max_cands) *
-                   static_cast<size_t>(p->num_heads) * 512));
-      a.plan = plan;
-      CandArgs pa;
-      std::memset(&pa, 0, sizeof(pa));
-      pa.offsets = a.offsets;
-      pa.cand_offsets = cand_offsets;
-      pa.timestamps = a.timestamps;
-      pa.cand_ts = cand_timestamps;
-      pa.plan = plan;
-      pa.plan_j = 4 * ((p->max_seq_len + 127) / 128);
-      pa.status = a.status;
-      pa.B = a.B;
-      pa.T = a.T;
-      pa.C = a.C;
-      pa.H = a.H;
-      pa.max_tiles = (max_cands + 127) / 128;
-      pa.max_seq_len = a.max_seq_len;
-      pa.bt = a.bt;
-      err = launch_cand_plans(pa, cs);   // the time-plan shapes, once for all heads
+      uint8_t* plans = static_cast<uint8_t*>(workspace) + kStatusBytes +
+                       align_up(cand4_part_rows(p->batch, p->num_heads, p->max_seq_len, total_cands, max_cands) *
+                                static_cast<size_t>(p->num_heads) * 512);
+      a.plan = reinterpret_cast<uint32_t*>(plans);
+      a.near = reinterpret_cast<uint4*>(plans + cand4_near_offset(p->max_seq_len, total_cands));
+      err = launch_cand4_plans(a, cs);   // once for all heads
     }
     if (err == cudaSuccess) err = launch_cand4_sm100(a, tq, cs);
   } else if (hist) {

@@ -29,6 +29,8 @@ struct Proj8Outs {
   CUtensorMap map[4];
 };
 
+constexpr int kCand4Near = 4;
+
 // Arguments of candidate scoring against histories in a 4-bit cache (kv4.cu
 // has the cache's layout).
 struct Cand4Args {
@@ -53,7 +55,12 @@ struct Cand4Args {
   // workspace: sums over the history, [slices][C][H*128] fp32; a slice is the
   // part of a history that one warp (many candidates: one CTA) walks
   float* part;
-  const uint32_t* plan;          // many candidates, with a time table: CandArgs::plan
+  // workspace (many candidates, with a time table): the time plan of every
+  // candidate against every 32-key block of its user's history, a word each,
+  // [blocks][C]; and, for the last kCand4Near blocks where the plan is TB_GEN32,
+  // the bucket of every score, a byte each, [kCand4Near][C][32]
+  uint32_t* plan;
+  uint4* near;
   int* status;
   int B, T, C, H, R;
   int max_seq_len, max_cands;
@@ -80,9 +87,11 @@ Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands, int total_token
 // bytes of the many-candidate kernel's time plans: both grow with each of them.
 size_t cand4_part_rows(int B, int H, int max_seq_len, int C, int max_cands);
 size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands);
+size_t cand4_near_offset(int max_seq_len, int C);   // of Cand4Args::near behind the plans
 
 // Kernel launchers (return cudaSuccess or the launch error).
 cudaError_t launch_cand4_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t stream);
+cudaError_t launch_cand4_plans(const Cand4Args& a, cudaStream_t stream);
 cudaError_t launch_cand4_sm100(const Cand4Args& a, const CUtensorMap& tq, cudaStream_t stream);
 cudaError_t launch_cand4_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_sums,
                                 cudaStream_t stream);

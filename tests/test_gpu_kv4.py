@@ -280,6 +280,17 @@ def test_many_users(B, most, cands):
     check(c, c.call())
 
 
+@pytest.mark.parametrize("cands", [(5, 2), (90, 170)])
+def test_timestamps_in_any_order(cands):
+    """Histories whose timestamps do not ascend, candidates before, among and
+    after them: every bucket is looked up by itself."""
+    c = Case(21, [333, 260], list(cands), 4)
+    for s, e in ((0, 333), (333, 593)):
+        c.ts[s:e] = c.ts[s:e][torch.randperm(e - s, generator=gen(2)).to(DEV)]
+    c.cts -= torch.randint(0, 2_000_000, (sum(cands),), generator=gen(3)).to(DEV)
+    check(c, c.call())
+
+
 def test_users_share_rows():
     """Two users over the same cache rows score as two copies would."""
     c = Case(8, [200, 200], [3, 5], 4, time=False)
