@@ -393,6 +393,26 @@ def test_two_streams_with_their_own_workspaces():
         assert all(torch.equal(w, y) for y in ys)
 
 
+@pytest.mark.parametrize("H", [3, 8])
+@pytest.mark.parametrize("cands", [(2, 1, 3), (60, 20, 130)])
+def test_free_rows_may_hold_anything(cands, H):
+    """Cache rows between the users' hold NaN scales and any codes."""
+    c = Case(23, [45, 130, 1], list(cands), H, scattered=True)
+    used = torch.zeros(c.cache[0].shape[0], dtype=torch.bool, device=DEV)
+    for first, n in zip(c.first_rows.tolist(), c.lens):
+        used[first:first + n] = True
+    for t in c.cache:
+        t[~used] = float("nan") if t.dtype == BF16 else 255
+    check(c, c.call())
+
+
+@pytest.mark.parametrize("cands", [(2, 1), (60, 20)])
+def test_lengths_far_below_the_bound(cands):
+    """max_seq_len bounds the histories; here it is a thousand times theirs."""
+    c = Case(22, [150, 77], list(cands), 2, pos=False)
+    check(c, c.call(max_len=150_000))
+
+
 def test_extreme_scores():
     """Biases at the type's lowest value give weight 0, also where they cover a
     whole history."""

@@ -221,6 +221,44 @@ def test_outputs_over_inputs():
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("dtype,E", [(BF16, 512), (F32, 100), (F32, 33), (BF16, 2048)])
+def test_more_outputs_over_inputs(dtype, E):
+    """The stream over x, the norm over the residual; y and 8 bits from one
+    call; dx over dy."""
+    x, res = rows(1, 50, E, dtype), rows(2, 50, E, dtype)
+    want = pa.hstu_rmsnorm_fwd(x, residual=res, eps=EPS, save_rstd=True)
+    q = pa.hstu_rmsnorm_fwd(x, residual=res, eps=EPS, quant=True)
+    a, b = x.clone(), res.clone()
+    got = pa.hstu_rmsnorm_fwd(a, residual=b, eps=EPS, quant=True, out=dict(h=a, y=b))
+    assert torch.equal(got["h"], want["h"]) and got["h"].data_ptr() == a.data_ptr()
+    assert torch.equal(got["y"], want["y"]) and got["y"].data_ptr() == b.data_ptr()
+    assert torch.equal(got["q8"].float(), q["q8"].float()) and torch.equal(got["scale"], q["scale"])
+    dy = rows(3, 50, E, dtype)
+    dx, dw = pa.hstu_rmsnorm_bwd(dy, want["h"], want["rstd"], d_residual=res)
+    d2 = dy.clone()
+    dx2, dw2 = pa.hstu_rmsnorm_bwd(d2, want["h"], want["rstd"], d_residual=res, dx=d2)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+def test_a_given_stream_and_wrong_arguments():
+    x = rows(1, 40, 256, BF16)
+    want = pa.hstu_rmsnorm_fwd(x, eps=EPS)["y"]
+    s = torch.cuda.Stream()
+    y = torch.empty_like(x)
+    s.wait_stream(torch.cuda.current_stream())
+    pa.hstu_rmsnorm_fwd(x, eps=EPS, out=dict(y=y), stream=s)
+    s.synchronize()
+    assert torch.equal(y, want)
+    for bad in (lambda: pa.hstu_rmsnorm_fwd(x.t()), lambda: pa.hstu_rmsnorm_fwd(x[0]),
+                lambda: pa.hstu_rmsnorm_fwd(x, residual=x.float()),
+                lambda: pa.hstu_rmsnorm_fwd(x, weight=torch.ones(255, device=DEV)),
+                lambda: pa.hstu_rmsnorm_fwd(x.half()),
+                lambda: pa.hstu_rmsnorm_bwd(x, x, torch.ones(39, device=DEV)),
+                lambda: pa.hstu_quant_rows(x[:, :128])):
+        with pytest.raises(ValueError):
+            bad()
+
+
 # ------------------------------------------------------------ 8-bit projection
 def silu64(x):
     return x / (1.0 + torch.exp(-x))
@@ -263,9 +301,10 @@ def test_uvqk_fp8(T, E, H, dqk, dv, act, bias):
     project(T + E, T, E, H, dqk, dv, act, bias, "uvqk")
 
 
-@pytest.mark.parametrize("T", [1111, 5000, 40001])
-def test_uvqk_fp8_many_rows(T):
-    project(T, T, 192, 4, 128, 128, 1, True, "uvqk")
+@pytest.mark.parametrize("T,E", [(1111, 192), (1250, 192), (5000, 192), (40001, 192), (1300, 1024),
+                                 (5000, 1024), (3000, 1536)])
+def test_uvqk_fp8_many_rows(T, E):
+    project(T, T, E, 4, 128, 128, 1, True, "uvqk")
 
 
 def test_uvqk_fp8_outputs_stay_inside(monkeypatch):
