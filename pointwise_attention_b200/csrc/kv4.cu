@@ -18,8 +18,8 @@
 //
 // Both directions move 2 * 256 B of bf16 and 2 * 72 B of cache per token and
 // head, once: HBM bounds them.  Measured on a B200, 69637 tokens of 8 heads (365
-// MB each way): 168 us for both, 4.4 TB/s (one word a thread, divisions and
-// one-element arithmetic: 407 us).
+// MB each way): 145 us for both, 5.0 TB/s (one word a thread, divisions and
+// one-element arithmetic: 407 us; four words a thread: 168 us).
 #include <cuda_bf16.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -28,12 +28,17 @@
 #include "hstu.h"
 #include "internal.h"
 #include "kv4.cuh"
+#include "ptx.cuh"
 
 namespace hstu {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWords = 4;   // words of a thread, kThreads apart: that many loads in flight
+// A thread takes pairs of words (16 values: 32 bytes of bf16, 8 of codes), so
+// that its loads or stores fill whole sectors, kPairs of them kThreads apart:
+// that many loads are in flight.  With single words the reading back was bound
+// by L1 (90% busy).
+constexpr int kPairs = 4;
 
 struct Kv4Args {
   const void* src[2];    // pack: k, v bf16 [T, H, 128]; unpack: codes
@@ -41,18 +46,19 @@ struct Kv4Args {
   void* scales[2];       // written by pack, read by unpack
   const int32_t* rows;   // [T] cache row of each token, or null (token t: row t)
   int* status;
-  int64_t units;         // T * H * 16 words of eight values
+  int64_t units;         // T * H * 8 pairs of words
   int H, R;              // heads, cache rows
+  int vec32;             // k and v are 32-byte aligned
 };
 
-// Word i of the call: token i / (16 H), and the same word of its cache row.
+// Pair i of the call: token i / (8 H), and the same pair of its cache row.
 // Rows outside the cache: -1 marks a token that has none; others are reported.
-__device__ __forceinline__ bool cache_word(const Kv4Args& a, int64_t i, int64_t* at) {
+__device__ __forceinline__ bool cache_pair(const Kv4Args& a, int64_t i, int64_t* at) {
   if (!a.rows) {
     *at = i;
     return true;
   }
-  const int64_t per = 16ll * a.H, t = i / per;
+  const int64_t per = 8ll * a.H, t = i / per;
   const int row = __ldg(a.rows + t);
   if (row < 0 || row >= a.R) {
     if (row != -1 && a.status) atomicOr(a.status, kStatusBadOffsets);
@@ -62,67 +68,79 @@ __device__ __forceinline__ bool cache_word(const Kv4Args& a, int64_t i, int64_t*
   return true;
 }
 
-// Four neighbouring lanes share a group of 32.
+// Two neighbouring lanes share a group of 32.
 __global__ void __launch_bounds__(kThreads) hstu_kv4_pack_rows(const Kv4Args a) {
   const int which = static_cast<int>(blockIdx.y);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kWords) + threadIdx.x;
-  uint4 raw[kWords];
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kPairs) + threadIdx.x;
+  const uint4* src = static_cast<const uint4*>(a.src[which]);
+  uint32_t w[kPairs][8];
 #pragma unroll
-  for (int j = 0; j < kWords; ++j) {
-    const int64_t i = i0 + j * kThreads;   // units is a multiple of 16: whole groups of lanes
-    raw[j] = i < a.units ? __ldg(static_cast<const uint4*>(a.src[which]) + i)
-                         : make_uint4(0u, 0u, 0u, 0u);
+  for (int j = 0; j < kPairs; ++j) {
+    const int64_t i = i0 + j * kThreads;   // units is a multiple of 8: whole groups of lanes
+    if (i < a.units && a.vec32) {
+      ld_global_nc_v8(src + 2 * i, w[j]);
+    } else {
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 lo = i < a.units ? __ldg(src + 2 * i) : zero, hi = i < a.units ? __ldg(src + 2 * i + 1) : zero;
+      w[j][0] = lo.x; w[j][1] = lo.y; w[j][2] = lo.z; w[j][3] = lo.w;
+      w[j][4] = hi.x; w[j][5] = hi.y; w[j][6] = hi.z; w[j][7] = hi.w;
+    }
   }
 #pragma unroll
-  for (int j = 0; j < kWords; ++j) {
+  for (int j = 0; j < kPairs; ++j) {
     const int64_t i = i0 + j * kThreads;
-    const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
     // |x| as bit patterns: ordered like the values, NaN above infinity; the
     // maximum of both halves of a word at once
-    uint32_t m = w[0] & 0x7FFF7FFFu;
+    uint32_t m = w[j][0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int e = 1; e < 4; ++e) m = __vmaxu2(m, w[e] & 0x7FFF7FFFu);
+    for (int e = 1; e < 8; ++e) m = __vmaxu2(m, w[j][e] & 0x7FFF7FFFu);
     m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const float s = kv4_scale(max(m >> 16, m & 0xFFFFu));
     const float inv = kv4_inverse(s);
     const uint64_t inv2 = pack_f32x2(inv, inv);
-    uint32_t code = 0;
+    uint32_t code[2] = {0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) code |= (kv4_codes(w[e], inv2) & 0x000F000Fu) << (4 * e);
+    for (int e = 0; e < 8; ++e)
+      code[e >> 2] |= (kv4_codes(w[j][e], inv2) & 0x000F000Fu) << (4 * (e & 3));
     int64_t at;
-    if (i >= a.units || !cache_word(a, i, &at)) continue;
-    static_cast<uint32_t*>(a.dst[which])[at] = code;
-    if ((at & 3) == 0)
-      static_cast<__nv_bfloat16*>(a.scales[which])[at >> 2] = __float2bfloat16_rn(s);   // exact
+    if (i >= a.units || !cache_pair(a, i, &at)) continue;
+    static_cast<uint2*>(a.dst[which])[at] = make_uint2(code[0], code[1]);
+    if ((at & 1) == 0)
+      static_cast<__nv_bfloat16*>(a.scales[which])[at >> 1] = __float2bfloat16_rn(s);   // exact
   }
 }
 
 __global__ void __launch_bounds__(kThreads) hstu_kv4_unpack_rows(const Kv4Args a) {
   const int which = static_cast<int>(blockIdx.y);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kWords) + threadIdx.x;
-  uint32_t code[kWords], scale[kWords];
-  bool live[kWords];
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kPairs) + threadIdx.x;
+  uint2 code[kPairs];
+  uint32_t scale[kPairs];
+  bool live[kPairs];
 #pragma unroll
-  for (int j = 0; j < kWords; ++j) {
+  for (int j = 0; j < kPairs; ++j) {
     const int64_t i = i0 + j * kThreads;
     int64_t at;
-    live[j] = i < a.units && cache_word(a, i, &at);
+    live[j] = i < a.units && cache_pair(a, i, &at);
     if (live[j]) {
-      code[j] = __ldg(static_cast<const uint32_t*>(a.src[which]) + at);
-      scale[j] = __ldg(static_cast<const uint16_t*>(a.scales[which]) + (at >> 2));
+      code[j] = __ldg(static_cast<const uint2*>(a.src[which]) + at);
+      scale[j] = __ldg(static_cast<const uint16_t*>(a.scales[which]) + (at >> 1));
     }
   }
 #pragma unroll
-  for (int j = 0; j < kWords; ++j) {
+  for (int j = 0; j < kPairs; ++j) {
     if (!live[j]) continue;
     const uint32_t s2 = scale[j] | (scale[j] << 16);
-    uint4 o;
-    o.x = kv4_pair<0>(code[j], s2);
-    o.y = kv4_pair<1>(code[j], s2);
-    o.z = kv4_pair<2>(code[j], s2);
-    o.w = kv4_pair<3>(code[j], s2);
-    static_cast<uint4*>(a.dst[which])[i0 + j * kThreads] = o;
+    const uint32_t o[8] = {kv4_pair<0>(code[j].x, s2), kv4_pair<1>(code[j].x, s2),
+                           kv4_pair<2>(code[j].x, s2), kv4_pair<3>(code[j].x, s2),
+                           kv4_pair<0>(code[j].y, s2), kv4_pair<1>(code[j].y, s2),
+                           kv4_pair<2>(code[j].y, s2), kv4_pair<3>(code[j].y, s2)};
+    uint4* dst = static_cast<uint4*>(a.dst[which]) + 2 * (i0 + j * kThreads);
+    if (a.vec32) {
+      st_global_v8(dst, o);
+    } else {
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
   }
 }
 
@@ -141,8 +159,8 @@ hstu_status_t run(bool pack, int32_t T, int32_t H, int32_t cache_rows, const int
       if (!p || reinterpret_cast<uintptr_t>(p) % 16 != 0) return HSTU_ERR_INVALID_ARG;
   }
   if (reinterpret_cast<uintptr_t>(rows) % 4 != 0) return HSTU_ERR_INVALID_ARG;
-  // blocks of kThreads * kWords words in grid x
-  const int64_t units = 16ll * T * H;
+  // blocks of kThreads * kPairs pairs of words in grid x
+  const int64_t units = 8ll * T * H;
   if (H > 65536 || units > 0x7FFFFFFFll * kThreads) return HSTU_ERR_UNSUPPORTED;
   // only the cache rows given by index can be found wrong on the device
   if ((rows || workspace) && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0 ||
@@ -161,7 +179,8 @@ hstu_status_t run(bool pack, int32_t T, int32_t H, int32_t cache_rows, const int
   a.units = units;
   a.H = H;
   a.R = cache_rows;
-  constexpr int64_t kBlock = kThreads * kWords;
+  a.vec32 = reinterpret_cast<uintptr_t>(k) % 32 == 0 && reinterpret_cast<uintptr_t>(v) % 32 == 0;
+  constexpr int64_t kBlock = kThreads * kPairs;
   const dim3 grid(static_cast<unsigned>((units + kBlock - 1) / kBlock), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pack)

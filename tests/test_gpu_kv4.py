@@ -108,6 +108,19 @@ def test_rows_holes_and_bad_rows():
     assert all(torch.equal(a, b) for a, b in zip(before, cache))
 
 
+def test_keys_off_32_bytes():
+    """k, v and the tensors read into on 16 bytes, not 32."""
+    T, H = 19, 3
+    k, v = rnd(1, T, H, 128), rnd(2, T, H, 128)
+    want = pa.hstu_kv4_pack(k, v)
+    off = lambda t: torch.cat([t.new_zeros(8), t.flatten()])[8:].view(t.shape)
+    got = pa.hstu_kv4_pack(off(k), off(v))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    out = (off(torch.zeros_like(k)), off(torch.zeros_like(v)))
+    pa.hstu_kv4_unpack(got, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(out, pa.hstu_kv4_unpack(want)))
+
+
 def test_infinities_and_nan_stay_in_their_group():
     k, v = rnd(1, 4, 2, 128), rnd(2, 4, 2, 128)
     clean = pa.hstu_kv4_unpack(pa.hstu_kv4_pack(k, v))
