@@ -18,7 +18,7 @@
 //
 // Both directions move 2 * 256 B of bf16 and 2 * 72 B of cache per token and
 // head, once: HBM bounds them.  Measured on a B200, 69637 tokens of 8 heads (365
-// MB each way): 145 us for both, 5.0 TB/s (one word a thread, divisions and
+// MB each way): 135 us for both, 5.4 TB/s (one word a thread, divisions and
 // one-element arithmetic: 407 us; four words a thread: 168 us).
 #include <cuda_bf16.h>
 #include <nvtx3/nvToolsExt.h>
@@ -33,12 +33,16 @@
 namespace hstu {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 // A thread takes pairs of words (16 values: 32 bytes of bf16, 8 of codes), so
-// that its loads or stores fill whole sectors, kPairs of them kThreads apart:
-// that many loads are in flight.  With single words the reading back was bound
-// by L1 (90% busy).
-constexpr int kPairs = 4;
+// that its loads or stores fill whole sectors, P of them kThreads apart: that
+// many loads are in flight.  With single words the reading back was bound by
+// L1 (90% busy).  P is 8, or 1 where blocks of 8 would leave SMs without one
+// (both ways, 8 heads, one kernel after the other in a graph: 32 tokens 2.8 us
+// with P = 1 and 6.0 with 8, 2048 tokens 11.0 and 8.0, 69637 tokens 256 and
+// 133; 4 and 16 pairs 141 and 145 there).
+constexpr int kPairs = 8;
+constexpr int kSms = 148;
 
 struct Kv4Args {
   const void* src[2];    // pack: k, v bf16 [T, H, 128]; unpack: codes
@@ -69,13 +73,14 @@ __device__ __forceinline__ bool cache_pair(const Kv4Args& a, int64_t i, int64_t*
 }
 
 // Two neighbouring lanes share a group of 32.
+template <int P>
 __global__ void __launch_bounds__(kThreads) hstu_kv4_pack_rows(const Kv4Args a) {
   const int which = static_cast<int>(blockIdx.y);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kPairs) + threadIdx.x;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * P) + threadIdx.x;
   const uint4* src = static_cast<const uint4*>(a.src[which]);
-  uint32_t w[kPairs][8];
+  uint32_t w[P][8];
 #pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
+  for (int j = 0; j < P; ++j) {
     const int64_t i = i0 + j * kThreads;   // units is a multiple of 8: whole groups of lanes
     if (i < a.units && a.vec32) {
       ld_global_nc_v8(src + 2 * i, w[j]);
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) hstu_kv4_pack_rows(const Kv4Args a) 
     }
   }
 #pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
+  for (int j = 0; j < P; ++j) {
     const int64_t i = i0 + j * kThreads;
     // |x| as bit patterns: ordered like the values, NaN above infinity; the
     // maximum of both halves of a word at once
@@ -110,14 +115,15 @@ __global__ void __launch_bounds__(kThreads) hstu_kv4_pack_rows(const Kv4Args a) 
   }
 }
 
+template <int P>
 __global__ void __launch_bounds__(kThreads) hstu_kv4_unpack_rows(const Kv4Args a) {
   const int which = static_cast<int>(blockIdx.y);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kPairs) + threadIdx.x;
-  uint2 code[kPairs];
-  uint32_t scale[kPairs];
-  bool live[kPairs];
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * P) + threadIdx.x;
+  uint2 code[P];
+  uint32_t scale[P];
+  bool live[P];
 #pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
+  for (int j = 0; j < P; ++j) {
     const int64_t i = i0 + j * kThreads;
     int64_t at;
     live[j] = i < a.units && cache_pair(a, i, &at);
@@ -127,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) hstu_kv4_unpack_rows(const Kv4Args a
     }
   }
 #pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
+  for (int j = 0; j < P; ++j) {
     if (!live[j]) continue;
     const uint32_t s2 = scale[j] | (scale[j] << 16);
     const uint32_t o[8] = {kv4_pair<0>(code[j].x, s2), kv4_pair<1>(code[j].x, s2),
@@ -159,7 +165,7 @@ hstu_status_t run(bool pack, int32_t T, int32_t H, int32_t cache_rows, const int
       if (!p || reinterpret_cast<uintptr_t>(p) % 16 != 0) return HSTU_ERR_INVALID_ARG;
   }
   if (reinterpret_cast<uintptr_t>(rows) % 4 != 0) return HSTU_ERR_INVALID_ARG;
-  // blocks of kThreads * kPairs pairs of words in grid x
+  // blocks of at least kThreads pairs of words in grid x
   const int64_t units = 8ll * T * H;
   if (H > 65536 || units > 0x7FFFFFFFll * kThreads) return HSTU_ERR_UNSUPPORTED;
   // only the cache rows given by index can be found wrong on the device
@@ -180,13 +186,13 @@ hstu_status_t run(bool pack, int32_t T, int32_t H, int32_t cache_rows, const int
   a.H = H;
   a.R = cache_rows;
   a.vec32 = reinterpret_cast<uintptr_t>(k) % 32 == 0 && reinterpret_cast<uintptr_t>(v) % 32 == 0;
-  constexpr int64_t kBlock = kThreads * kPairs;
-  const dim3 grid(static_cast<unsigned>((units + kBlock - 1) / kBlock), 2);
+  const int64_t many = (units + kThreads * kPairs - 1) / (kThreads * kPairs);
+  const bool few = 2 * many < kSms;
+  const dim3 grid(static_cast<unsigned>(few ? (units + kThreads - 1) / kThreads : many), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pack)
-    hstu_kv4_pack_rows<<<grid, kThreads, 0, s>>>(a);
-  else
-    hstu_kv4_unpack_rows<<<grid, kThreads, 0, s>>>(a);
+  const auto kernel = pack ? (few ? hstu_kv4_pack_rows<1> : hstu_kv4_pack_rows<kPairs>)
+                           : (few ? hstu_kv4_unpack_rows<1> : hstu_kv4_unpack_rows<kPairs>);
+  kernel<<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 

@@ -121,6 +121,36 @@ def test_keys_off_32_bytes():
     assert all(torch.equal(a, b) for a, b in zip(out, pa.hstu_kv4_unpack(want)))
 
 
+@pytest.mark.parametrize("T,H", [(4001, 3), (9473, 1), (1700, 8)])
+def test_long_calls_are_the_calls_of_their_parts(T, H):
+    """Calls that fill the GPU against calls of a few tokens, bit for bit:
+    packed in order, packed to rows in another order with holes, read back."""
+    k, v = rnd(7, T, H, 128, std=3.0), rnd(8, T, H, 128)
+    parts = [pa.hstu_kv4_pack(k[i:i + 500].contiguous(), v[i:i + 500].contiguous())
+             for i in range(0, T, 500)]
+    want = [torch.cat(t) for t in zip(*parts)]
+    got = pa.hstu_kv4_pack(k, v)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    R = T + 77
+    rows = torch.randperm(R, generator=torch.Generator().manual_seed(9))[:T].int().cuda()
+    rows[::5] = -1
+    live = rows >= 0
+    cache = [torch.full((R, *t.shape[1:]), 3, dtype=t.dtype, device="cuda") for t in want]
+    expect = [t.clone() for t in cache]
+    for e, w in zip(expect, want):
+        e[rows[live].long()] = w[live]
+    pa.hstu_kv4_pack(k, v, cache=cache, rows=rows)
+    assert all(torch.equal(a, b) for a, b in zip(cache, expect))
+
+    out = (torch.full_like(k, 5.0), torch.full_like(v, 5.0))
+    pa.hstu_kv4_unpack(cache, rows=rows, out=out)
+    whole = pa.hstu_kv4_unpack(want)
+    for o, w in zip(out, whole):
+        assert torch.equal(o[live], w[live])
+        assert bool((o[~live] == 5.0).all())
+
+
 def test_infinities_and_nan_stay_in_their_group():
     k, v = rnd(1, 4, 2, 128), rnd(2, 4, 2, 128)
     clean = pa.hstu_kv4_unpack(pa.hstu_kv4_pack(k, v))
