@@ -20,8 +20,12 @@
 // to h, 8 bits, scales and rstd, 471 MB: 80 us (5.9 TB/s; 90 us with the next
 // row's loads in registers, 128 us with one-element arithmetic, whose 470
 // instructions a row were what bounded it); backward of 32768 x 512 bf16 with
-// d_residual, 134 MB: 37 us with the kernel of the weight's sums (3.6 TB/s: nine
-// rows a warp; 45 us without the ring).
+// d_residual, 134 MB: 31 us with the kernel of the weight's sums (4.4 TB/s; 37 us
+// with three blocks an SM, whose 80 registers a thread spill; 45 us without the
+// ring).  2^25 elements in rows of other lengths, before and after those lengths
+// had shapes of their own, in us: bf16 forward 64 columns 115 -> 49, 333 125 ->
+// 88, 8000 68 -> 50, 8001 176 -> 80; bf16 backward 64 columns 137 -> 50, 4096
+// 75 -> 52, 8001 173 -> 92; fp32 backward 512 columns 98 -> 68, 8192 100 -> 76.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <nvtx3/nvToolsExt.h>
@@ -132,7 +136,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 // threads of a row.  TPR > 32: the block is the row.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = warp_sum(v);
+#pragma unroll
+  for (int o = TPR < 32 ? TPR / 2 : 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (TPR > 32) {
     __syncthreads();   // red may still be read by the row before
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -146,7 +151,12 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 
 template <int TPR>
 __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
-  v = __reduce_max_sync(0xffffffffu, v);
+  if (TPR < 32) {
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  } else {
+    v = __reduce_max_sync(0xffffffffu, v);
+  }
   if (TPR > 32) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -159,7 +169,17 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
 }
 
 template <int TPR>
-constexpr int block_threads() { return TPR == 32 ? 256 : TPR; }
+constexpr int block_threads() { return TPR <= 32 ? 256 : TPR; }
+
+// Blocks of an SM that a kernel of N elements a thread is compiled for: up to 24
+// warps, backward 16 where 24 would spill (32768 x 512 bf16: 31 against 37 us).
+template <int TPR, int N>
+constexpr int fwd_resident() { return N <= 16 ? 768 / block_threads<TPR>() : 1; }
+template <int TPR, int N>
+constexpr int bwd_resident() {
+  constexpr int blocks = (N <= 8 ? 768 : N <= 16 ? 512 : 256) / block_threads<TPR>();
+  return blocks > 0 ? blocks : 1;
+}
 
 // The arithmetic runs on pairs of neighbouring owned elements (fp32 pairs: one
 // instruction for two), which halves the issue slots that bound these kernels
@@ -189,25 +209,32 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// Rows on their way from HBM: where a warp owns a row and takes it in 16-byte
-// vectors, it copies the rows that it will come to asynchronously to shared
-// memory, kDepth - 1 rows ahead.  Every lane copies what it reads itself, so its
-// own wait for its copies is all that stands between the two.
-template <typename T, int VEC, int TPR, int NV, int TENSORS>
+// Rows on their way from HBM: where they are taken in 16-byte vectors, a
+// thread copies its part of the rows that it will come to asynchronously to
+// shared memory, kDepth - 1 rows ahead: as many as BLOCKS blocks of an SM have
+// room for.  Every thread copies what it reads itself, so its own wait for its
+// copies is all that stands between the two.
+template <typename T, int VEC, int TPR, int NV, int TENSORS, int BLOCKS>
 struct Ring {
-  static constexpr bool on = VEC > 1 && TPR == 32;
-  static constexpr int kDepth = NV <= 4 ? 3 : 2;
-  static constexpr int kBytes = on ? 8 * kDepth * TENSORS * NV * 512 : 0;   // 8 rows a block
-  uint4* mine;   // of this lane: [stage][tensor][vector], 32 vectors apart
-  int lane, E, stage;
+  static constexpr int kRows = block_threads<TPR>() / TPR;
+  static constexpr int kStage = kRows * TENSORS * NV * TPR * 16;
+  static constexpr int kRoom = 227 * 1024 / BLOCKS - 1536;   // beside a block's own kilobyte
+  static constexpr int kDepth = NV <= 4 && 3 * kStage <= kRoom ? 3 : 2;
+  // (forward: one row ahead is what its registers hold without the ring, and a
+  // block per row is no faster with a ring of two: 2048 fp32 98 against 93 us)
+  static constexpr bool on =
+      VEC > 1 && kDepth * kStage <= kRoom && (TPR <= 32 || TENSORS == 3 || kDepth == 3);
+  static constexpr int kBytes = on ? kDepth * kStage : 0;
+  uint4* mine;   // of this thread: [stage][tensor][vector], TPR vectors apart
+  int lane, stage;
 
-  __device__ __forceinline__ Ring(void* smem, int sub, int lane_, int E_)
-      : mine(static_cast<uint4*>(smem) + (sub * kDepth * TENSORS * NV) * 32 + lane_),
-        lane(lane_), E(E_), stage(0) {}
+  __device__ __forceinline__ Ring(void* smem, int sub, int lane_)
+      : mine(static_cast<uint4*>(smem) + (sub * kDepth * TENSORS * NV) * TPR + lane_),
+        lane(lane_), stage(0) {}
   __device__ __forceinline__ uint4* slot(int st, int tensor, int i) const {
-    return mine + ((st * TENSORS + tensor) * NV + i) * 32;
+    return mine + ((st * TENSORS + tensor) * NV + i) * TPR;
   }
-  __device__ __forceinline__ void copy(int st, int tensor, const T* row) const {
+  __device__ __forceinline__ void copy(int st, int tensor, const T* row, int E) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * VEC;
@@ -222,7 +249,7 @@ struct Ring {
   __device__ __forceinline__ static void wait() {   // all but the newest kDepth - 2 groups
     asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
   }
-  __device__ __forceinline__ void read(int tensor, Pack<T, VEC> (&p)[NV]) const {
+  __device__ __forceinline__ void read(int tensor, Pack<T, VEC> (&p)[NV], int E) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((i * TPR + lane) * VEC < E) {
@@ -237,13 +264,13 @@ struct Ring {
 
 // NORM: the norm; otherwise the rows as they are (quantisation alone).
 template <typename T, int VEC, int TPR, int NV, bool NORM>
-__global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / block_threads<TPR>() : 1)
+__global__ void __launch_bounds__(block_threads<TPR>(), fwd_resident<TPR, NV * VEC>())
     hstu_rows_fwd(const RowsArgs a) {
   constexpr int kRows = block_threads<TPR>() / TPR;   // rows of a block at a time
   constexpr int N = NV * VEC, P = N / 2;
   __shared__ float red[TPR > 32 ? TPR / 32 : 1];
-  const int lane = TPR == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-  const int sub = TPR == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  const int lane = static_cast<int>(threadIdx.x) % TPR;
+  const int sub = static_cast<int>(threadIdx.x) / TPR;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.res);
   uint64_t w[P];
@@ -253,40 +280,47 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
 #pragma unroll
     for (int i = 0; i < P; ++i) w[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
   }
-  // The loop is uniform over the threads of a row, and over the block where
-  // the block is the row.  Without the ring the next row's loads are issued
-  // before this row's sums are waited for.
+  // The loop is uniform over a warp, and over the block where the block is the
+  // row; rows past T of a warp with several read as zeros and are not written.
+  // Without the ring the next row's loads are issued before this row's sums
+  // are waited for.
   const int stride = static_cast<int>(gridDim.x) * kRows;
   int t = static_cast<int>(blockIdx.x) * kRows + sub;
   Pack<T, VEC> p[NV], q[NV];
   auto load = [&](int row) {
-    load_row<T, VEC, TPR, NV>(x + static_cast<size_t>(row) * a.E, lane, a.E, p);
-    if (NORM && res) load_row<T, VEC, TPR, NV>(res + static_cast<size_t>(row) * a.E, lane, a.E, q);
+    const int E = row < a.T ? a.E : 0;
+    load_row<T, VEC, TPR, NV>(x + static_cast<size_t>(row) * a.E, lane, E, p);
+    if (NORM && res) load_row<T, VEC, TPR, NV>(res + static_cast<size_t>(row) * a.E, lane, E, q);
   };
-  using R = Ring<T, VEC, TPR, NV, 2>;
+  using R = Ring<T, VEC, TPR, NV, 2, fwd_resident<TPR, N>()>;
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  R ring(s_dyn, sub, lane, a.E);
-  auto send = [&](int row, int st) {   // rows past T are not copied; their group is empty
-    if (row < a.T) {
-      ring.copy(st, 0, x + static_cast<size_t>(row) * a.E);
-      if (NORM && res) ring.copy(st, 1, res + static_cast<size_t>(row) * a.E);
+  R ring(s_dyn, sub, lane);
+  // rows past T are not copied; their group is empty (rows ahead may pass 31 bits)
+  auto send = [&](uint32_t row, int st) {
+    if (row < static_cast<uint32_t>(a.T)) {
+      ring.copy(st, 0, x + static_cast<size_t>(row) * a.E, a.E);
+      if (NORM && res) ring.copy(st, 1, res + static_cast<size_t>(row) * a.E, a.E);
     }
     R::commit();
   };
   if constexpr (R::on) {
 #pragma unroll
-    for (int i = 0; i < R::kDepth - 1; ++i) send(t + i * stride, i);
+    for (int i = 0; i < R::kDepth - 1; ++i) send(static_cast<uint32_t>(t) + i * stride, i);
   } else {
-    if (t < a.T) load(t);
+    if (TPR < 32 || t < a.T) load(t);
   }
-  for (; t < a.T; t += stride) {
+  // the first row of the warp
+  int tw = TPR < 32 ? t - sub % (TPR < 32 ? 32 / TPR : 1) : t;
+  for (; tw < a.T; t += stride, tw += stride) {
+    const bool live = TPR >= 32 || t < a.T;
+    const int E = live ? a.E : 0;
     const size_t at = static_cast<size_t>(t) * a.E;
     if constexpr (R::on) {
       R::wait();
-      ring.read(0, p);
-      if (NORM && res) ring.read(1, q);
+      ring.read(0, p, E);
+      if (NORM && res) ring.read(1, q, E);
       // the stage of the row before is free
-      send(t + (R::kDepth - 1) * stride, ring.stage == 0 ? R::kDepth - 1 : ring.stage - 1);
+      send(static_cast<uint32_t>(t) + (R::kDepth - 1) * stride, ring.stage == 0 ? R::kDepth - 1 : ring.stage - 1);
       ring.stage = ring.stage == R::kDepth - 1 ? 0 : ring.stage + 1;
     }
     if (NORM && res) {
@@ -298,14 +332,14 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = (i * TPR + lane) * VEC;
-          if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(h + c) = p[i];
+          if (c < E) *reinterpret_cast<Pack<T, VEC>*>(h + c) = p[i];
         }
       }
     }
     uint64_t v[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = get_pair<T, VEC, NV>(p, i);
-    if (!R::on && t < a.T - stride) load(t + stride);
+    if (!R::on && tw < a.T - stride) load(t + stride);
     if (NORM) {
       uint64_t ss2 = 0ull;
 #pragma unroll
@@ -313,7 +347,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
       const float2 s2 = unpack_f32x2(ss2);
       const float ss = row_sum<TPR>(s2.x + s2.y, red);
       const float r = 1.0f / sqrtf(ss / static_cast<float>(a.E) + a.eps);
-      if (a.rstd && lane == 0) a.rstd[t] = r;
+      if (a.rstd && lane == 0 && live) a.rstd[t] = r;
       const uint64_t r2 = pack_f32x2(r, r);
 #pragma unroll
       for (int i = 0; i < P; ++i) v[i] = fmul2(fmul2(v[i], r2), w[i]);
@@ -325,7 +359,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = (i * TPR + lane) * VEC;
-          if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(y + c) = o[i];
+          if (c < E) *reinterpret_cast<Pack<T, VEC>*>(y + c) = o[i];
         }
       }
     }
@@ -343,7 +377,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
           __uint_as_float(row_umax<TPR>(__float_as_uint(m), reinterpret_cast<uint32_t*>(red)));
       const float s = (top < kAmaxFloor ? kAmaxFloor : top) / kE4M3Max;
       const float inv = 1.0f / s;
-      if (lane == 0) a.scale[t] = s;
+      if (lane == 0 && live) a.scale[t] = s;
       uint8_t* q8 = a.q8 + at;
       const uint64_t inv2 = pack_f32x2(inv, inv);
       Pack<uint8_t, VEC> o[NV];
@@ -361,23 +395,23 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + lane) * VEC;
-        if (c < a.E) *reinterpret_cast<Pack<uint8_t, VEC>*>(q8 + c) = o[i];
+        if (c < E) *reinterpret_cast<Pack<uint8_t, VEC>*>(q8 + c) = o[i];
       }
     }
   }
 }
 
 template <typename T, int VEC, int TPR, int NV>
-__global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / block_threads<TPR>() : 1)
+__global__ void __launch_bounds__(block_threads<TPR>(), bwd_resident<TPR, NV * VEC>())
     hstu_rows_bwd(const RowsBwdArgs a) {
   constexpr int kRows = block_threads<TPR>() / TPR;
   constexpr int N = NV * VEC, P = N / 2;
   __shared__ float red[TPR > 32 ? TPR / 32 : 1];
-  // the rows' ring and, after the rows, the warps' weight sums [kRows][32 N]
+  // the rows' ring and, after the rows, their weight sums [kRows][TPR N]
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  using R = Ring<T, VEC, TPR, NV, 3>;
-  const int lane = TPR == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-  const int sub = TPR == 32 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  using R = Ring<T, VEC, TPR, NV, 3, bwd_resident<TPR, N>()>;
+  const int lane = static_cast<int>(threadIdx.x) % TPR;
+  const int sub = static_cast<int>(threadIdx.x) / TPR;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   uint64_t w[P], dw2[P];
   {
@@ -395,38 +429,43 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
   const T* dy = static_cast<const T*>(a.dy);
   const T* h = static_cast<const T*>(a.h);
   const T* dres = static_cast<const T*>(a.dres);
-  R ring(s_dyn, sub, lane, a.E);
-  auto send = [&](int row, int st) {   // rows past T are not copied; their group is empty
-    if (row < a.T) {
+  R ring(s_dyn, sub, lane);
+  // rows past T are not copied; their group is empty (rows ahead may pass 31 bits)
+  auto send = [&](uint32_t row, int st) {
+    if (row < static_cast<uint32_t>(a.T)) {
       const size_t at = static_cast<size_t>(row) * a.E;
-      ring.copy(st, 0, dy + at);
-      ring.copy(st, 1, h + at);
-      if (dres) ring.copy(st, 2, dres + at);
+      ring.copy(st, 0, dy + at, a.E);
+      ring.copy(st, 1, h + at, a.E);
+      if (dres) ring.copy(st, 2, dres + at, a.E);
     }
     R::commit();
   };
   float rn = t < a.T ? __ldg(a.rstd + t) : 0.f;
   if constexpr (R::on) {
 #pragma unroll
-    for (int i = 0; i < R::kDepth - 1; ++i) send(t + i * stride, i);
+    for (int i = 0; i < R::kDepth - 1; ++i) send(static_cast<uint32_t>(t) + i * stride, i);
   }
-  for (; t < a.T; t += stride) {
+  // the first row of the warp
+  int tw = TPR < 32 ? t - sub % (TPR < 32 ? 32 / TPR : 1) : t;
+  for (; tw < a.T; t += stride, tw += stride) {
+    const bool live = TPR >= 32 || t < a.T;
+    const int E = live ? a.E : 0;
     const size_t at = static_cast<size_t>(t) * a.E;
     if constexpr (R::on) {
       R::wait();
-      ring.read(0, pd);
-      ring.read(1, ph);
-      if (dres) ring.read(2, pr);
+      ring.read(0, pd, E);
+      ring.read(1, ph, E);
+      if (dres) ring.read(2, pr, E);
       // the stage of the row before is free
-      send(t + (R::kDepth - 1) * stride, ring.stage == 0 ? R::kDepth - 1 : ring.stage - 1);
+      send(static_cast<uint32_t>(t) + (R::kDepth - 1) * stride, ring.stage == 0 ? R::kDepth - 1 : ring.stage - 1);
       ring.stage = ring.stage == R::kDepth - 1 ? 0 : ring.stage + 1;
     } else {
-      load_row<T, VEC, TPR, NV>(dy + at, lane, a.E, pd);
-      load_row<T, VEC, TPR, NV>(h + at, lane, a.E, ph);
-      if (dres) load_row<T, VEC, TPR, NV>(dres + at, lane, a.E, pr);
+      load_row<T, VEC, TPR, NV>(dy + at, lane, E, pd);
+      load_row<T, VEC, TPR, NV>(h + at, lane, E, ph);
+      if (dres) load_row<T, VEC, TPR, NV>(dres + at, lane, E, pr);
     }
     const float r = rn;
-    if (t < a.T - stride) rn = __ldg(a.rstd + t + stride);
+    rn = t < a.T - stride ? __ldg(a.rstd + t + stride) : 0.f;
     const uint64_t r2 = pack_f32x2(r, r);
     // g = w dy and z = h r: dx = r g - z (r mean(g z)), dw += dy z; g and z are
     // made twice, which leaves registers for more rows on an SM
@@ -454,7 +493,7 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * VEC;
-      if (c < a.E) *reinterpret_cast<Pack<T, VEC>*>(dx + c) = pd[i];
+      if (c < E) *reinterpret_cast<Pack<T, VEC>*>(dx + c) = pd[i];
     }
   }
   float dw[N];
@@ -466,18 +505,18 @@ __global__ void __launch_bounds__(block_threads<TPR>(), NV * VEC <= 16 ? 768 / b
   }
   if (!a.partial) return;
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * a.E;
-  if (TPR == 32) {
-    // the warps' sums of the block, added in warp order, over the ring's room
+  if (TPR <= 32) {
+    // the sums of the block's rows, added in their order, over the ring's room
     float* sdw = reinterpret_cast<float*>(s_dyn);
     if constexpr (R::on) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) sdw[sub * 32 * N + (i / VEC * 32 + lane) * VEC + i % VEC] = dw[i];
+    for (int i = 0; i < N; ++i) sdw[sub * TPR * N + (i / VEC * TPR + lane) * VEC + i % VEC] = dw[i];
     __syncthreads();
     for (int c = static_cast<int>(threadIdx.x); c < a.E; c += block_threads<TPR>()) {
       float s = 0.f;
 #pragma unroll
-      for (int g = 0; g < kRows; ++g) s += sdw[g * 32 * N + c];
+      for (int g = 0; g < kRows; ++g) s += sdw[g * TPR * N + c];
       part[c] = s;
     }
   } else {
@@ -519,10 +558,10 @@ __global__ void __launch_bounds__(1024) hstu_rows_dw(const float* partial, int b
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // One row shape of the kernels: elements per vector, threads per row, vectors
-// per thread.  The smallest that holds E columns is taken: a warp per row up
-// to 1024 columns (8 rows a block, no barrier), 128 threads up to 4096, 512
-// up to 16384.  Rows whose columns or addresses do not divide into 16-byte
-// vectors take one element at a time.
+// per thread.  The smallest that holds E columns is taken: a part of a warp per
+// row for short rows, a warp up to 1024 columns (no barrier), 128 threads up to
+// 4096, 512 up to 16384.  Rows whose columns or addresses do not divide into
+// 16-byte vectors take one element at a time.
 template <int VEC_, int TPR_, int NV_>
 struct Shape {
   static constexpr int VEC = VEC_, TPR = TPR_, NV = NV_;
@@ -532,7 +571,10 @@ template <typename T, typename F>
 cudaError_t pick_shape(bool vec, int E, F&& f) {
   if constexpr (sizeof(T) == 2) {
     if (vec) {
-      if (E <= 256) return f(Shape<8, 32, 1>{});
+      if (E <= 32) return f(Shape<8, 4, 1>{});
+      if (E <= 64) return f(Shape<8, 8, 1>{});
+      if (E <= 128) return f(Shape<8, 8, 2>{});
+      if (E <= 256) return f(Shape<8, 16, 2>{});
       if (E <= 512) return f(Shape<8, 32, 2>{});
       if (E <= 1024) return f(Shape<8, 32, 4>{});
       if (E <= 2048) return f(Shape<8, 128, 2>{});
@@ -542,7 +584,10 @@ cudaError_t pick_shape(bool vec, int E, F&& f) {
     }
   } else {
     if (vec) {
-      if (E <= 128) return f(Shape<4, 32, 1>{});
+      if (E <= 16) return f(Shape<4, 4, 1>{});
+      if (E <= 32) return f(Shape<4, 8, 1>{});
+      if (E <= 64) return f(Shape<4, 16, 1>{});
+      if (E <= 128) return f(Shape<4, 16, 2>{});
       if (E <= 256) return f(Shape<4, 32, 2>{});
       if (E <= 512) return f(Shape<4, 32, 4>{});
       if (E <= 1024) return f(Shape<4, 32, 8>{});
@@ -552,10 +597,14 @@ cudaError_t pick_shape(bool vec, int E, F&& f) {
       return f(Shape<4, 512, 8>{});
     }
   }
+  if (E <= 64) return f(Shape<1, 8, 8>{});
+  if (E <= 128) return f(Shape<1, 16, 8>{});
   if (E <= 256) return f(Shape<1, 32, 8>{});
+  if (E <= 512) return f(Shape<1, 32, 16>{});
   if (E <= 1024) return f(Shape<1, 32, 32>{});
   if (E <= 2048) return f(Shape<1, 128, 16>{});
   if (E <= 4096) return f(Shape<1, 128, 32>{});
+  if (E <= 8192) return f(Shape<1, 512, 16>{});
   return f(Shape<1, 512, 32>{});
 }
 
@@ -563,7 +612,7 @@ cudaError_t pick_shape(bool vec, int E, F&& f) {
 // KIND tell the kernels apart).
 template <typename S, typename T, int KIND, typename K>
 cudaError_t opt_in(K kernel, int smem) {
-  if (smem <= 48 * 1024) return cudaSuccess;
+  if (smem <= 47 * 1024) return cudaSuccess;   // of 48, a little is static
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -587,8 +636,11 @@ cudaError_t launch_rows_fwd(const RowsArgs& a, cudaStream_t stream) {
     constexpr int kRows = block_threads<S::TPR>() / S::TPR;
     // eight blocks per SM at most: each row's loads then run ahead of it
     const int64_t need = (static_cast<int64_t>(a.T) + kRows - 1) / kRows;
-    const int blocks = static_cast<int>(need < 8 * 148 ? need : 8 * 148);
-    constexpr int smem = Ring<T, S::VEC, S::TPR, S::NV, 2>::kBytes;
+    // (and 2^16 rows: kMaxT)
+    const int most = 8 * 148 * kRows < 0x10000 ? 8 * 148 : 0xFFFF / kRows;
+    const int blocks = static_cast<int>(need < most ? need : most);
+    constexpr int smem =
+        Ring<T, S::VEC, S::TPR, S::NV, 2, fwd_resident<S::TPR, S::NV * S::VEC>()>::kBytes;
     auto kernel = hstu_rows_fwd<T, S::VEC, S::TPR, S::NV, NORM>;
     const cudaError_t err = opt_in<S, T, NORM ? 1 : 2>(kernel, smem);
     if (err != cudaSuccess) return err;
@@ -597,12 +649,13 @@ cudaError_t launch_rows_fwd(const RowsArgs& a, cudaStream_t stream) {
   });
 }
 
-// Blocks of the backward: enough rows each that the partial sums stay small
-// beside the rows.  A function of the sizes alone (not of the device), so that
+// Blocks of the backward: as many as run at a time, so that each starts and
+// adds its weight's sums once.  A function of the sizes alone (not of the device), so that
 // the order of the sums is too.
 int bwd_blocks(int T, int E) {
   const int rows = E <= 1024 ? 8 : 1;
-  const int most = E <= 1024 ? 3 * 148 : E <= 4096 ? 6 * 148 : 2 * 148;
+  const int most =
+      (E <= 64 ? 3 : E <= 512 ? 2 : E <= 1024 ? 1 : E <= 2048 ? 4 : E <= 4096 ? 2 : 1) * 148;
   const int64_t need = (static_cast<int64_t>(T) + rows - 1) / rows;
   return static_cast<int>(need < most ? need : most);
 }
@@ -615,8 +668,8 @@ cudaError_t launch_rows_bwd(const RowsBwdArgs& a, float* dw, cudaStream_t stream
   const int blocks = bwd_blocks(a.T, a.E);
   const cudaError_t err = pick_shape<T>(vec, a.E, [&](auto s) {
     using S = decltype(s);
-    using R = Ring<T, S::VEC, S::TPR, S::NV, 3>;
-    constexpr int sums = S::TPR == 32 ? 8 * 32 * S::NV * S::VEC * 4 : 0;
+    using R = Ring<T, S::VEC, S::TPR, S::NV, 3, bwd_resident<S::TPR, S::NV * S::VEC>()>;
+    constexpr int sums = S::TPR <= 32 ? 256 * S::NV * S::VEC * 4 : 0;
     constexpr int smem = R::kBytes > sums ? R::kBytes : sums;
     auto kernel = hstu_rows_bwd<T, S::VEC, S::TPR, S::NV>;
     const cudaError_t e = opt_in<S, T, 0>(kernel, smem);
@@ -701,7 +754,12 @@ HSTU_API hstu_status_t hstu_quant_rows(hstu_dtype_t dtype, int32_t T, int32_t E,
 
 HSTU_API size_t hstu_rmsnorm_bwd_workspace_size(int32_t T, int32_t E) {
   if (T < 0 || T > kMaxT || E < 1 || E > kMaxE) return 0;
-  const size_t n = static_cast<size_t>(bwd_blocks(T, E)) * E * sizeof(float);
+  // no less than smaller calls of any row length need
+  size_t n = static_cast<size_t>(bwd_blocks(T, E)) * E * sizeof(float);
+  for (int e = 256; e < E; e *= 2) {
+    const size_t m = static_cast<size_t>(bwd_blocks(T, e)) * e * sizeof(float);
+    if (m > n) n = m;
+  }
   return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
 

@@ -143,10 +143,7 @@ def test_norm_backward_many_rows_repeats_bitwise():
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
-@pytest.mark.parametrize("dtype,E", [(BF16, 24), (F32, 20), (BF16, 520), (F32, 7)])
-def test_many_rows_a_warp(dtype, E):
-    """Every warp walks several rows (more than are under way at a time)."""
-    T = 50021 if E < 500 else 30011
+def check_many_rows(T, E, dtype):
     x, res, dy = (rows(s, T, E, dtype) for s in (1, 2, 3))
     rel = (E + 16) * U
     h, rstd, v = norm64(x, res, None, dtype)
@@ -163,6 +160,63 @@ def test_many_rows_a_warp(dtype, E):
     tol = r * (dyd.abs() * 4 * U + hd.abs() * r * r * mabs * rel) + res.double().abs() * 2 * U
     within(dx, ref, tol + ref.abs() * (HALF[dtype] + 2 * U), "dx")
     terms = dyd * hd * r
+    within(dw, terms.sum(0), terms.abs().sum(0) * (T + 8) * U, "dw")
+
+
+@pytest.mark.parametrize("dtype,E", [(BF16, 24), (F32, 20), (BF16, 520), (F32, 7)])
+def test_many_rows_a_warp(dtype, E):
+    """Every warp walks several rows (more than are under way at a time)."""
+    check_many_rows(50021 if E < 500 else 30011, E, dtype)
+
+
+@pytest.mark.parametrize("T,E,dtype", [
+    (200003, 8, BF16), (150001, 64, BF16), (150001, 16, F32), (100003, 40, F32), (60001, 33, BF16),
+    (60001, 128, BF16), (60001, 65, F32), (50021, 256, BF16), (20011, 301, F32), (20011, 301, BF16),
+    (4801, 2048, BF16), (4801, 2048, F32), (4801, 4096, BF16), (4801, 4096, F32),
+    (4801, 8192, BF16), (4801, 8000, F32), (2411, 8001, F32), (2411, 16384, BF16)])
+def test_many_rows_of_every_shape(T, E, dtype):
+    check_many_rows(T, E, dtype)
+
+
+NARROW = [(1, 3), (2, 16), (3, 30), (5, 32), (515, 32), (37, 50), (9, 64), (70, 100), (13, 128),
+          (6, 136), (9, 200), (7, 300), (9, 333), (2, 2001), (2, 4001)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E", NARROW)
+def test_rows_narrower_than_a_warp(T, E, dtype):
+    test_norm_forward(T, E, dtype)
+    test_norm_backward(T, E, dtype)
+    test_quant_rows(T, E, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E", [(1, 16), (5, 32), (3, 64), (7, 128), (2, 50), (1, 512), (33, 24)])
+def test_rows_behind_the_last_stay(T, E, dtype):
+    """Rows and values past T of larger tensors hold NaN, which nothing reads,
+    and stay: a warp's rows may end inside it."""
+    R = T + 70
+    big = [rows(s, R, E, dtype) for s in (1, 2, 3)]
+    for t in big:
+        t[T:] = float("nan")
+    x, res, dy = (t[:T] for t in big)
+    outs = {k: torch.full((R, E), 7.0, dtype=dtype, device=DEV) for k in ("h", "y")}
+    outs["rstd"] = torch.full((R,), 7.0, device=DEV)
+    out = pa.hstu_rmsnorm_fwd(x, residual=res, eps=EPS, save_rstd=True,
+                              out={k: t[:T] for k, t in outs.items()})
+    h, _, v = norm64(x, res, None, dtype)
+    assert torch.equal(out["h"], h)
+    within(out["y"], v, v.abs() * (HALF[dtype] + 2 * (E + 16) * U), "y")
+    for t in outs.values():
+        assert bool((t[T:] == 7.0).all())
+    q8 = {"q8": torch.zeros(R, E, dtype=torch.float8_e4m3fn, device=DEV),
+          "scale": torch.full((R,), 7.0, device=DEV)}
+    pa.hstu_rmsnorm_fwd(x, residual=res, eps=EPS, quant=True, out={k: t[:T] for k, t in q8.items()})
+    assert bool((q8["scale"][T:] == 7.0).all()) and bool((q8["q8"][T:].float() == 0).all())
+    dx = torch.full((R, E), 7.0, dtype=dtype, device=DEV)
+    _, dw = pa.hstu_rmsnorm_bwd(dy, out["h"], out["rstd"], d_residual=res, dx=dx[:T])
+    assert bool((dx[T:] == 7.0).all()) and bool(torch.isfinite(dx).all())
+    terms = dy.double() * h.double() * out["rstd"].double()[:, None]
     within(dw, terms.sum(0), terms.abs().sum(0) * (T + 8) * U, "dw")
 
 
