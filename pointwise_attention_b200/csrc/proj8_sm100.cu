@@ -21,8 +21,9 @@
 // row per thread.  Every wait is bounded.
 //
 // Measured on a B200: 131072 x 512 by 2048 columns with SiLU, 605 MB, 275 GFLOP:
-// 156 us = 1.76 PFLOP/s = 3.9 TB/s (bf16 operands: 0.40 ms).  Shared memory
-// bounds it: operands, staged outputs and column scales keep it 84% busy.
+// 156 us = 1.76 PFLOP/s = 3.9 TB/s (bf16 operands: 0.40 ms).  The writes bound
+// it: a fill of the 537 MB of outputs alone takes 140 us; shared memory
+// (operands, staged outputs, column scales) is 84% busy.
 #include <cuda_bf16.h>
 
 #include <atomic>

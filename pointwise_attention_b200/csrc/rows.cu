@@ -17,10 +17,10 @@
 // backward read; y and q8 take v unrounded.
 //
 // Measured on a B200 (copies reach 6.56 TB/s): 131071 x 512 bf16 with a residual
-// to h, 8 bits, scales and rstd, 471 MB: 80 us (5.9 TB/s; 90 us with the next
+// to h, 8 bits, scales and rstd, 471 MB: 78 us (6.0 TB/s; 90 us with the next
 // row's loads in registers, 128 us with one-element arithmetic, whose 470
 // instructions a row were what bounded it); backward of 32768 x 512 bf16 with
-// d_residual, 134 MB: 31 us with the kernel of the weight's sums (4.4 TB/s; 37 us
+// d_residual, 134 MB: 27 us with the kernel of the weight's sums (5.0 TB/s; 31 us
 // with three blocks an SM, whose 80 registers a thread spill; 45 us without the
 // ring).  2^25 elements in rows of other lengths, before and after those lengths
 // had shapes of their own, in us: bf16 forward 64 columns 115 -> 49, 333 125 ->
@@ -172,7 +172,7 @@ template <int TPR>
 constexpr int block_threads() { return TPR <= 32 ? 256 : TPR; }
 
 // Blocks of an SM that a kernel of N elements a thread is compiled for: up to 24
-// warps, backward 16 where 24 would spill (32768 x 512 bf16: 31 against 37 us).
+// warps, backward 16 where 24 would spill (32768 x 512 bf16: 27 against 31 us).
 template <int TPR, int N>
 constexpr int fwd_resident() { return N <= 16 ? 768 / block_threads<TPR>() : 1; }
 template <int TPR, int N>
