@@ -119,6 +119,10 @@ __device__ __forceinline__ void load_weight(const float* w, int lane, int E, flo
           r[i * VEC + e + 2] = f.z;
           r[i * VEC + e + 3] = f.w;
         }
+      } else if (VEC == 2) {
+        const float2 f = __ldg(reinterpret_cast<const float2*>(w + c));
+        r[i * VEC] = f.x;
+        r[i * VEC + VEC - 1] = f.y;
       } else {
         r[i * VEC] = __ldg(w + c);
       }
@@ -223,7 +227,7 @@ struct Ring {
   // (forward: one row ahead is what its registers hold without the ring, and a
   // block per row is no faster with a ring of two: 2048 fp32 98 against 93 us)
   static constexpr bool on =
-      VEC > 1 && kDepth * kStage <= kRoom && (TPR <= 32 || TENSORS == 3 || kDepth == 3);
+      sizeof(T) * VEC == 16 && kDepth * kStage <= kRoom && (TPR <= 32 || TENSORS == 3 || kDepth == 3);
   static constexpr int kBytes = on ? kDepth * kStage : 0;
   uint4* mine;   // of this thread: [stage][tensor][vector], TPR vectors apart
   int lane, stage;
@@ -561,14 +565,17 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 // per thread.  The smallest that holds E columns is taken: a part of a warp per
 // row for short rows, a warp up to 1024 columns (no barrier), 128 threads up to
 // 4096, 512 up to 16384.  Rows whose columns or addresses do not divide into
-// 16-byte vectors take one element at a time.
+// 16-byte vectors take one element at a time; bf16 in pairs where the columns
+// are even and the addresses allow it, in the backward (2^25 elements, 334
+// columns 73 -> 64 us, 1002 68 -> 58, 8002 92 -> 75) and in short rows (forward
+// 50 columns 73 -> 60 us, 202 80 -> 71; 334 88 -> 98, so not there).
 template <int VEC_, int TPR_, int NV_>
 struct Shape {
   static constexpr int VEC = VEC_, TPR = TPR_, NV = NV_;
 };
 
-template <typename T, typename F>
-cudaError_t pick_shape(bool vec, int E, F&& f) {
+template <typename T, bool BWD, typename F>
+cudaError_t pick_shape(bool vec, bool pairs, int E, F&& f) {
   if constexpr (sizeof(T) == 2) {
     if (vec) {
       if (E <= 32) return f(Shape<8, 4, 1>{});
@@ -581,6 +588,19 @@ cudaError_t pick_shape(bool vec, int E, F&& f) {
       if (E <= 4096) return f(Shape<8, 128, 4>{});
       if (E <= 8192) return f(Shape<8, 512, 2>{});
       return f(Shape<8, 512, 4>{});
+    }
+    if (pairs && E <= 64) return f(Shape<2, 8, 4>{});
+    if (pairs && E <= 128) return f(Shape<2, 16, 4>{});
+    if (pairs && E <= 256) return f(Shape<2, 32, 4>{});
+    if constexpr (BWD) {
+      if (pairs) {
+        if (E <= 512) return f(Shape<2, 32, 8>{});
+        if (E <= 1024) return f(Shape<2, 32, 16>{});
+        if (E <= 2048) return f(Shape<2, 128, 8>{});
+        if (E <= 4096) return f(Shape<2, 128, 16>{});
+        if (E <= 8192) return f(Shape<2, 512, 8>{});
+        return f(Shape<2, 512, 16>{});
+      }
     }
   } else {
     if (vec) {
@@ -631,7 +651,9 @@ cudaError_t launch_rows_fwd(const RowsArgs& a, cudaStream_t stream) {
   const bool vec = a.E % (V / sizeof(T)) == 0 && aligned(a.x, V) && aligned(a.res, V) &&
                    aligned(a.h, V) && aligned(a.y, V) && aligned(a.q8, V / sizeof(T)) &&
                    aligned(a.weight, V);
-  return pick_shape<T>(vec, a.E, [&](auto s) {
+  const bool pairs = a.E % 2 == 0 && aligned(a.x, 4) && aligned(a.res, 4) && aligned(a.h, 4) &&
+                     aligned(a.y, 4) && aligned(a.q8, 2) && aligned(a.weight, 8);
+  return pick_shape<T, false>(vec, pairs, a.E, [&](auto s) {
     using S = decltype(s);
     constexpr int kRows = block_threads<S::TPR>() / S::TPR;
     // eight blocks per SM at most: each row's loads then run ahead of it
@@ -665,8 +687,10 @@ cudaError_t launch_rows_bwd(const RowsBwdArgs& a, float* dw, cudaStream_t stream
   constexpr size_t V = 16;
   const bool vec = a.E % (V / sizeof(T)) == 0 && aligned(a.dy, V) && aligned(a.h, V) &&
                    aligned(a.dres, V) && aligned(a.dx, V) && aligned(a.weight, V);
+  const bool pairs = a.E % 2 == 0 && aligned(a.dy, 4) && aligned(a.h, 4) && aligned(a.dres, 4) &&
+                     aligned(a.dx, 4) && aligned(a.weight, 8);
   const int blocks = bwd_blocks(a.T, a.E);
-  const cudaError_t err = pick_shape<T>(vec, a.E, [&](auto s) {
+  const cudaError_t err = pick_shape<T, true>(vec, pairs, a.E, [&](auto s) {
     using S = decltype(s);
     using R = Ring<T, S::VEC, S::TPR, S::NV, 3, bwd_resident<S::TPR, S::NV * S::VEC>()>;
     constexpr int sums = S::TPR <= 32 ? 256 * S::NV * S::VEC * 4 : 0;

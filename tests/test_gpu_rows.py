@@ -191,6 +191,52 @@ def test_rows_narrower_than_a_warp(T, E, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E", [(1, 2), (9, 22), (5, 66), (5, 130), (3, 258), (9, 514), (3, 1030),
+                                 (2, 2050), (2, 4098), (2, 8194), (1, 16382)])
+def test_rows_of_even_length(T, E, dtype):
+    test_norm_forward(T, E, dtype)
+    test_norm_backward(T, E, dtype)
+    test_quant_rows(T, E, dtype)
+
+
+@pytest.mark.parametrize("T,E", [(100003, 30), (60001, 100), (50021, 202), (20011, 500),
+                                 (9001, 1002), (4801, 2004), (4801, 4002), (2411, 8002)])
+def test_many_rows_of_even_length(T, E):
+    check_many_rows(T, E, BF16)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("off", [1, 2, 4])
+def test_rows_off_their_vectors(dtype, off):
+    """Rows that start `off` elements past a 16-byte boundary, and a weight that
+    does: the same results to the rounding's order of sums, bit for bit in h."""
+    T, E = 37, 64
+    def shift(t):
+        b = t.new_zeros(t.numel() + 8)
+        b[off:off + t.numel()] = t.flatten()
+        return b[off:off + t.numel()].view(t.shape)
+    x, res, dy = (shift(rows(s, T, E, dtype)) for s in (1, 2, 3))
+    w = shift(1.0 + 0.3 * rows(4, 1, E, F32)[0])
+    rel = (E + 16) * U
+    h, rstd, v = norm64(x, res, w, dtype)
+    out = pa.hstu_rmsnorm_fwd(x, residual=res, weight=w, eps=EPS, save_rstd=True)
+    assert torch.equal(out["h"], h)
+    within(out["y"], v, v.abs() * (HALF[dtype] + 2 * rel), "y")
+    q8, s = pa.hstu_quant_rows(x)
+    check_q8(q8, s, x.double(), E, "q8")
+    dx, dw = pa.hstu_rmsnorm_bwd(dy, h, out["rstd"], weight=w)
+    dx2, dw2 = pa.hstu_rmsnorm_bwd(dy.clone(), h.clone(), out["rstd"], weight=w.clone())
+    terms = dy.double() * h.double() * out["rstd"].double()[:, None]
+    within(dw, terms.sum(0), terms.abs().sum(0) * (T + 8) * U, "dw")
+    g, hd, r = dy.double() * w.double(), h.double(), out["rstd"].double()[:, None]
+    m, mabs = (g * hd).mean(1, keepdim=True), (g * hd).abs().mean(1, keepdim=True)
+    ref = r * (g - hd * r * r * m)
+    tol = r * (g.abs() * 4 * U + hd.abs() * r * r * mabs * rel) + ref.abs() * (HALF[dtype] + 2 * U)
+    within(dx, ref, tol, "dx")
+    within(dx2, ref, tol, "dx")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T,E", [(1, 16), (5, 32), (3, 64), (7, 128), (2, 50), (1, 512), (33, 24)])
 def test_rows_behind_the_last_stay(T, E, dtype):
     """Rows and values past T of larger tensors hold NaN, which nothing reads,
