@@ -26,7 +26,7 @@ LIB = os.path.join(HERE, "libhstu.so")
 SOURCES = ["hstu_api.cu", "fwd_sm100.cu", "bwd_sm100.cu", "plans.cu", "proj_sm100.cu", "cand_sm100.cu",
            "rows.cu", "proj8_sm100.cu", "rab.cu", "kv4.cu", "cand4_few.cu", "cand4_sm100.cu", "cand4_plans.cu",
            "simt.cu", "selftest.cu", "noalloc.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "tile_math.cuh", "bounds.cuh", "kv4.cuh", "ops.cuh", "internal_ops.h"]
+HEADERS = ["internal.h", "ptx.cuh", "tile_math.cuh", "bounds.cuh", "kv4.cuh", "ops.cuh", "internal_ops.h", "cand4_cut.h"]
 # The debug build: every data-derived index checked on the device (bounds.cuh).
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(HERE, "libhstu_debug.so")

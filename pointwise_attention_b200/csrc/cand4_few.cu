@@ -40,7 +40,6 @@
 // end (64 us); cp.async by the lanes cost 145 shared-memory wavefronts a block.
 #include <cuda_bf16.h>
 
-#include <algorithm>
 #include <atomic>
 
 #include "bounds.cuh"
@@ -53,9 +52,9 @@
 namespace hstu {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = kCand4FewWarps;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxShare = 512;
+constexpr int kMaxShare = kCand4MaxShare;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -467,8 +466,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (8 * n + 2 * t + c >= cands) continue;
-        float4* dst = reinterpret_cast<float4*>(
-            a.part + (static_cast<size_t>(piece) * a.max_cands + 8 * n + 2 * t + c) * (a.H * 128) + h * 128 + 16 * g);
+        const size_t row = checked(a.status, static_cast<size_t>(piece) * a.max_cands + 8 * n + 2 * t + c,
+                                   a.part_rows, BS_CAND4_SUM);
+        float4* dst = reinterpret_cast<float4*>(a.part + row * (a.H * 128) + h * 128 + 16 * g);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           dst[i] = make_float4(o[n][2 * i][c], o[n][2 * i][c + 2], o[n][2 * i + 1][c], o[n][2 * i + 1][c + 2]);
@@ -617,7 +617,8 @@ __global__ void __launch_bounds__(256) hstu_cand4_finish_rows(const __grid_const
                 static_cast<int>(threadIdx.x >> 5);
   const int lane = static_cast<int>(threadIdx.x & 31);
   const User us = user_ranges(a, b);
-  if (!us.ok) {
+  const int cfirst = __ldg(a.cand_offsets);
+  if (!us.ok || !cand4_in_sums(us.c0, us.cb, cfirst, a.sum_rows)) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadOffsets);
     return;
   }
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(256) hstu_cand4_finish_rows(const __grid_const
   }
   const float inv_n = 1.0f / static_cast<float>(a.norm_len > 0 ? a.norm_len : us.nb + 1);
   const int slices = (us.nb + cut.chunk - 1) / cut.chunk;
-  const size_t stride = static_cast<size_t>(a.C) * D;
+  const size_t sum0 = static_cast<size_t>(us.c0 - cfirst + i);
   uint2 v[NH];
 #pragma unroll
   for (int h = 0; h < NH; ++h) v[h] = row2(a.v, h);
@@ -663,7 +664,8 @@ __global__ void __launch_bounds__(256) hstu_cand4_finish_rows(const __grid_const
 #pragma unroll
   for (int h = 0; h < NH; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = 0; s < slices; ++s) {
-    const float* src = a.part + s * stride + at;
+    const float* src =
+        a.part + checked(a.status, static_cast<size_t>(s) * a.sum_rows + sum0, a.part_rows, BS_CAND4_SUM) * D + 4 * lane;
     float4 f[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h)
@@ -767,59 +769,6 @@ cudaError_t launch_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t str
 }
 
 }  // namespace
-
-// More candidates per user than this take the tcgen05 kernel: for 32 users, 8
-// heads and 2176 keys, up to 7 candidates take 43 us and up to 15 take 70 us
-// here, and up to 23 take 150 us there, as much as two passes here would.
-constexpr int kFewMax = 16;
-
-Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands, int total_tokens) {
-  Cand4Cut c{};
-  c.many = max_cands > kFewMax;
-  if (c.many) {
-    c.parts = 1;
-    c.hgroups = H;
-    c.cgroups = static_cast<int>((static_cast<int64_t>(max_cands) + 255) / 256);
-    // one CTA walks a whole history where there are CTAs enough; otherwise
-    // histories are cut so that there are about two a SM
-    const int64_t groups = static_cast<int64_t>(B) * H * c.cgroups;
-    const int64_t want = groups > 2 * 148 ? 1 : (2 * 148 + groups - 1) / (groups > 0 ? groups : 1);
-    int64_t chunk = ((max_seq_len + want - 1) / want + 127) / 128 * 128;
-    if (chunk < 256) chunk = 256;
-    c.chunk = static_cast<int>(chunk);
-    c.splits = static_cast<int>((max_seq_len + chunk - 1) / chunk);
-    return c;
-  }
-  c.heads = H < kWarps ? H : kWarps;
-  c.parts = kWarps / c.heads;
-  c.hgroups = (H + kWarps - 1) / kWarps;
-  c.nt = max_cands <= 8 ? 1 : 2;
-  c.cgroups = 1;
-  // two CTAs a SM, or as many as keep the shares at kMaxShare tokens
-  const int64_t most = std::min(static_cast<int64_t>(B) * max_seq_len,
-                                static_cast<int64_t>(total_tokens));
-  c.ctas = static_cast<int>(std::max<int64_t>(2 * 148 / c.hgroups, (most + kMaxShare - 1) / kMaxShare));
-  return c;
-}
-
-// Few candidates: a row per candidate, part and piece; pieces begin with a CTA
-// or with a user.  Many: splits <= max_seq_len / 256 + 1, and splits <= 296 /
-// groups + 1 with C <= 256 groups / H.
-size_t cand4_part_rows(int B, int H, int max_seq_len, int C, int max_cands) {
-  const int64_t n = max_seq_len, c = C;
-  const Cand4Cut f = cand4_cut(B, H, max_seq_len, std::min(max_cands, kFewMax), 0x7FFFFFFF);
-  const int64_t few = (static_cast<int64_t>(f.ctas) + B) * f.parts * std::min(max_cands, kFewMax);
-  const int64_t many = std::min(c * (n / 256 + 1), c + 2 * 148 * 256 / H + 1);
-  return static_cast<size_t>(max_cands > kFewMax ? std::max(few, many) : few);
-}
-
-size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands) {
-  return max_cands > kFewMax ? cand4_near_offset(max_seq_len, C) + static_cast<size_t>(C) * 32 * kCand4Near : 0;
-}
-
-size_t cand4_near_offset(int max_seq_len, int C) {
-  return ((static_cast<size_t>(max_seq_len) + 31) / 32 * 4 * C + 255) / 256 * 256;
-}
 
 cudaError_t launch_cand4_finish(const Cand4Args& a, const Cand4Cut& cut, bool after_sums,
                                 cudaStream_t stream) {

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rank of the user), batches fastest: the batches of one (user, head) run at
   // the same time and share its cache rows in L2.
   struct Item {
-    int h, c0, cand0, rows, s, nb, r0, split, key0, keys, nt, tiles;
+    int h, c0, cand0, cfirst, rows, s, nb, r0, split, key0, keys, nt, tiles;
   };
   auto item_of = [&](unsigned round, Item& it) {   // false: nothing to do
     const unsigned base = round * gridDim.x;
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.h = static_cast<int>(x % static_cast<unsigned>(a.H));
     const int rank = static_cast<int>(x / static_cast<unsigned>(a.H));
     const int b = ordered ? order[rank] : rank;
+    it.cfirst = __ldg(a.cand_offsets);
     it.c0 = __ldg(a.cand_offsets + b);
     const int cb = __ldg(a.cand_offsets + b + 1) - it.c0;
     it.s = __ldg(a.offsets + b);
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ranges that contradict the sizes are reported by the last kernel
     if (it.c0 < 0 || cb < 0 || cb > a.C - it.c0 || cb > a.max_cands || it.s < 0 || it.nb < 0 ||
         it.nb > a.T - it.s || it.nb > a.max_seq_len || it.r0 < 0 || it.nb > a.R - it.r0 ||
-        (POS && it.nb >= a.L))
+        (POS && it.nb >= a.L) || !cand4_in_sums(it.c0, cb, it.cfirst, a.sum_rows))
       return false;
     it.key0 = it.split * a.chunk;
     it.keys = min(it.nb - it.key0, a.chunk);
@@ -592,7 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       Item it;
       item_of(round, it);
-      float* dst = a.part + (static_cast<size_t>(it.split) * a.C + cand) * D + it.h * 128;
+      const size_t row = checked(a.status, static_cast<size_t>(it.split) * a.sum_rows + (cand - it.cfirst),
+                                 a.part_rows, BS_CAND4_SUM);
+      float* dst = a.part + row * D + it.h * 128;
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t ov[32];

@@ -827,6 +827,8 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
   a.eps = p->ln_eps;
   a.chunk = cut.chunk;
   a.splits = cut.splits;
+  a.part_rows = cand4_part_rows(p->batch, p->num_heads, p->max_seq_len, total_cands, max_cands);
+  a.sum_rows = cand4_sum_rows(p->batch, total_cands, max_cands);
   if (p->rab_time) fill_bucket_table(&a.bt, p->num_time_buckets);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool hist = p->total_tokens > 0 && p->max_seq_len > 0;
@@ -836,8 +838,7 @@ hstu_status_t hstu_cand_kv4_fwd(const hstu_problem_t* p, const void* k_codes, co
     if (!make_map_3d(&tq, q, total_cands, p->num_heads, 128)) return HSTU_ERR_CUDA;
     if (p->rab_time) {
       uint8_t* plans = static_cast<uint8_t*>(workspace) + kStatusBytes +
-                       align_up(cand4_part_rows(p->batch, p->num_heads, p->max_seq_len, total_cands, max_cands) *
-                                static_cast<size_t>(p->num_heads) * 512);
+                       align_up(a.part_rows * static_cast<size_t>(p->num_heads) * 512);
       a.plan = reinterpret_cast<uint32_t*>(plans);
       a.near = reinterpret_cast<uint4*>(plans + cand4_near_offset(p->max_seq_len, total_cands));
       err = launch_cand4_plans(a, cs);   // once for all heads

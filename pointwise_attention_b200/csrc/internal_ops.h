@@ -1,12 +1,13 @@
 // internal_ops.h -- declarations of the 8-bit projection and of scoring against
 // the 4-bit cache, shared by the host API and their kernels.
 #pragma once
+#include "cand4_cut.h"
 #include "internal.h"
 
 namespace hstu {
 
 // Check sites of the HSTU_DEBUG_BOUNDS build (bounds.cuh has the others').
-constexpr int BS_CAND4_TS = 50, BS_CAND4_ROW = 51, BS_CAND4_KEY = 52;
+constexpr int BS_CAND4_TS = 50, BS_CAND4_ROW = 51, BS_CAND4_KEY = 52, BS_CAND4_SUM = 53;
 
 // Arguments of the UVQK projection of 8-bit rows.
 struct Proj8Args {
@@ -29,8 +30,6 @@ struct Proj8Outs {
   CUtensorMap map[4];
 };
 
-constexpr int kCand4Near = 4;
-
 // Arguments of candidate scoring against histories in a 4-bit cache (kv4.cu
 // has the cache's layout).
 struct Cand4Args {
@@ -52,9 +51,11 @@ struct Cand4Args {
   void* y;                       // candidates [C, H*128]
   const float* ln_weight;        // [H*128] or nullptr
   const float* ln_bias;
-  // workspace: sums over the history, [slices][C][H*128] fp32; a slice is the
-  // part of a history that one warp (many candidates: one CTA) walks
+  // workspace: sums over the history, [part_rows][H*128] fp32 (cand4_cut.h has
+  // which row is whose)
   float* part;
+  size_t part_rows;
+  int sum_rows;                  // many candidates: rows of a split's sums
   // workspace (many candidates, with a time table): the time plan of every
   // candidate against every 32-key block of its user's history, a word each,
   // [blocks][C]; and, for the last kCand4Near blocks where the plan is TB_GEN32,
@@ -69,25 +70,6 @@ struct Cand4Args {
   float eps;
   BucketTable bt;
 };
-
-// How a problem is cut (sizes alone decide).
-struct Cand4Cut {
-  int many;      // the kernel for many candidates: 256 of them, a head a CTA
-  int heads;     // few: heads of a CTA, one warp each, times
-  int parts;     // few: warps that share a head's keys (many: 1)
-  int hgroups;   // CTAs along the heads
-  int nt;        // few: groups of 8 candidates of a CTA
-  int ctas;      // few: shares of the tokens
-  int cgroups;   // many: CTAs along a user's candidates
-  int chunk, splits;   // many: history keys per CTA, CTAs along the longest history
-};
-Cand4Cut cand4_cut(int B, int H, int max_seq_len, int max_cands, int total_tokens);
-// Rows (of H*128 fp32) that hold the sums of every cut with H heads, at most B
-// histories of max_seq_len and at most C candidates, max_cands a user, and the
-// bytes of the many-candidate kernel's time plans: both grow with each of them.
-size_t cand4_part_rows(int B, int H, int max_seq_len, int C, int max_cands);
-size_t cand4_plan_bytes(int max_seq_len, int C, int max_cands);
-size_t cand4_near_offset(int max_seq_len, int C);   // of Cand4Args::near behind the plans
 
 // Kernel launchers (return cudaSuccess or the launch error).
 cudaError_t launch_cand4_few(const Cand4Args& a, const Cand4Cut& cut, cudaStream_t stream);
