@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_plans = [&](int n) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (128 * n + 32 * i < keys) pw[i] = __ldg(plan + static_cast<size_t>(i) * a.C);
+          if (128 * n + 32 * i < keys) pw[i] = ld_global_u32(plan + static_cast<size_t>(i) * a.C);
         plan += static_cast<size_t>(4) * a.C;
       };
       if (TIME && round_first) {
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p_block<POS, TB_MULTI>(sv, pos, ts32, tv, tp.s, my32, tab, packed);
               } else if (tb == TB_GEN32 && near0 - (4 * n + cc) < kCand4Near) {
                 const uint4* src = a.near + (static_cast<size_t>(near0 - (4 * n + cc)) * a.C + cand) * 2;
-                const uint4 lo = __ldg(src), hi = __ldg(src + 1);
+                const uint4 lo = ld_global_v4(src), hi = ld_global_v4(src + 1);
                 const uint32_t bytes[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                 p_block<POS, TB_BYTES>(sv, pos, bytes, tv, tp.s, my32, tab, packed);
               } else if (tb == TB_GEN32) {

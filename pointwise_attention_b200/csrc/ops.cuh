@@ -47,6 +47,22 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 
+// Loads of what another grid wrote while this one was already running (kept
+// behind griddepcontrol.wait, volatile as they are; the non-coherent path wants memory that nobody
+// writes as long as the kernel runs).
+__device__ __forceinline__ uint32_t ld_global_u32(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_global_v4(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // Untiled copy global -> shared of a multiple of 16 bytes between 16-byte
 // aligned addresses, completion counted in bytes on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
