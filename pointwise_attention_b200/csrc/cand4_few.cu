@@ -89,6 +89,15 @@ __device__ __forceinline__ void grid_dependents() {
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Before a thread of the last kernel leaves with nothing to do: the grid's first
+// block stays until the kernels before are over, so that this kernel ends after
+// them whatever the ranges are.  The next call on the workspace starts behind
+// this kernel alone, and the pass over the timestamps may still be at work for
+// users whose ranges this one reports.
+__device__ __forceinline__ void leave_last() {
+  if (blockIdx.x == 0) grid_wait();
+}
+
 // A round of a piece: 16 keys per part, brought to shared memory by bulk copies
 // (whole cache rows, which need no address arithmetic of the threads), kStages
 // - 1 rounds ahead.
@@ -506,9 +515,9 @@ __global__ void __launch_bounds__(1024) hstu_cand4_finish(const __grid_constant_
   const int share = share_of(a, cut);
   if (!us.ok || !in_shares(us, share, cut)) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadOffsets);
-    return;
+    return leave_last();
   }
-  if (i >= us.cb) return;
+  if (i >= us.cb) return leave_last();
   const int D = a.H * 128;
   const size_t cand = checked(a.status, us.c0 + i, a.C, BS_CAND4_ROW);
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
@@ -620,9 +629,9 @@ __global__ void __launch_bounds__(256) hstu_cand4_finish_rows(const __grid_const
   const int cfirst = __ldg(a.cand_offsets);
   if (!us.ok || !cand4_in_sums(us.c0, us.cb, cfirst, a.sum_rows)) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadOffsets);
-    return;
+    return leave_last();
   }
-  if (i >= us.cb) return;
+  if (i >= us.cb) return leave_last();
   const int D = a.H * 128;
   const size_t cand = checked(a.status, us.c0 + i, a.C, BS_CAND4_ROW);
   const size_t at = cand * D + 4 * lane;     // head h: + 128 h

@@ -58,3 +58,34 @@ def test_time_plans_are_those_of_the_call():
     assert pa.hstu_attn_check(ws) == 0
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 2]), i
+
+
+@pytest.mark.parametrize("m", [4, 130])
+def test_a_call_behind_one_that_reports_every_user(m):
+    """A call whose users all begin outside the cache writes nothing and is
+    reported; the call behind it on the workspace is not touched by what its
+    kernels still do."""
+    bad, good = Batch(21, 8, 3000, m, 4), Batch(31, 8, 3000, m, 4)
+    want = good.call(good.workspace())
+    ws = good.workspace()
+    nowhere = torch.full_like(bad.first, bad.cache[0].shape[0])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        bad.call(ws, first=nowhere)
+        got = good.call(ws)
+        assert pa.hstu_attn_check(ws) == pa._binding.HSTU_ERR_INVALID_ARG
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("m", [4, 130])
+def test_a_call_behind_one_without_candidates(m):
+    """No user has a candidate: nothing is written, and the next call is whole."""
+    none, good = Batch(41, 5, 2000, m, 4), Batch(51, 5, 2000, m, 4)
+    want = good.call(good.workspace())
+    ws = good.workspace()
+    none.coff = torch.zeros_like(none.coff)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        none.call(ws)
+        assert torch.equal(good.call(ws), want)
+    assert pa.hstu_attn_check(ws) == 0
