@@ -436,13 +436,30 @@ def _arg(t, name, dtype, *shape):
     raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
 
 
-def _on(ref, *tensors):
-    """A context in which ref's device is current; every tensor must be there."""
+def _on(ref, *tensors, stream=None):
+    """A context in which ref's device and the given stream are current; every
+    tensor must be there.  What a call allocates and clears in it (outputs,
+    workspace) is then ordered with its kernels, and is not handed out again
+    before them."""
     at = ref.get_device()
     for t in tensors:
         if t is not None and t.get_device() != at:
             raise ValueError("all tensors must be on one device (%s and %s)" % (ref.device, t.device))
+    if stream is not None:
+        if stream.device.index != at:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, ref.device))
+        return torch.cuda.stream(stream)
     return _STAY if torch._C._cuda_getDevice() == at else torch.cuda.device(at)
+
+
+def _hand_over(stream, *outputs):
+    """Outputs allocated on the given stream, for the caller's: their memory waits
+    for what the caller's stream has done with them when they are let go of."""
+    if stream is not None:
+        mine = torch.cuda.current_stream(stream.device)
+        for t in outputs:
+            if t is not None and mine != stream:
+                t.record_stream(mine)
 
 
 def _stream_of(ref, stream):
@@ -482,7 +499,8 @@ def hstu_rmsnorm_fwd(x, *, residual=None, weight=None, eps: float = 1e-6, quant:
         qp, sp = _arg(q8, "q8", _F8, T, E), _arg(scale, "scale", _F32, T)
         np_ = _arg(rstd, "rstd", _F32, T)
         _on(x, h, y, q8, scale, rstd)
-    with _on(x, residual, weight):
+    given = (h, y, q8, scale, rstd)
+    with _on(x, residual, weight, stream=stream):
         if residual is not None and h is None:
             h = torch.empty_like(x)
             hp = h.data_ptr()
@@ -503,6 +521,8 @@ def hstu_rmsnorm_fwd(x, *, residual=None, weight=None, eps: float = 1e-6, quant:
                                   _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rmsnorm_fwd")
+    if stream is not None:
+        _hand_over(stream, *(t for t, g in zip((h, y, q8, scale, rstd), given) if t is not g))
     return dict(h=h, y=y, q8=q8, scale=scale, rstd=rstd)
 
 
@@ -516,7 +536,8 @@ def hstu_rmsnorm_bwd(dy, h, rstd, *, weight=None, d_residual=None, need_weight_g
     args = (_arg(dy, "dy", dy.dtype), _arg(h, "h", dy.dtype, T, E), _arg(rstd, "rstd", _F32, T),
             _arg(weight, "weight", _F32, E), _arg(d_residual, "d_residual", dy.dtype, T, E))
     dxp = _arg(dx, "dx", dy.dtype, T, E)
-    with _on(dy, h, rstd, weight, d_residual, dx, workspace):
+    new = dx is None
+    with _on(dy, h, rstd, weight, d_residual, dx, workspace, stream=stream):
         if dx is None:
             dx = torch.empty_like(dy)
             dxp = dx.data_ptr()
@@ -534,6 +555,7 @@ def hstu_rmsnorm_bwd(dy, h, rstd, *, weight=None, d_residual=None, need_weight_g
                                   _stream_of(dy, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rmsnorm_bwd")
+    _hand_over(stream, dx if new else None, dw)
     return dx, dw
 
 
@@ -544,13 +566,14 @@ def hstu_quant_rows(x, *, stream=None):
     dt = _rows_dtype(x, "x")
     T, E = x.shape
     xp = _arg(x, "x", x.dtype)
-    with _on(x):
+    with _on(x, stream=stream):
         q8 = torch.empty_like(x, dtype=_F8)
         scale = x.new_empty(T, dtype=_F32)
         rc = lib.hstu_quant_rows(dt, T, E, xp, q8.data_ptr(), scale.data_ptr(),
                                  _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_quant_rows")
+    _hand_over(stream, q8, scale)
     return q8, scale
 
 
@@ -570,7 +593,8 @@ def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: 
         outs = out["u"], out["v"], out["q"], out["k"]
         ptrs = [_arg(t, n, _BF16, *sh) for t, n, sh in zip(outs, "uvqk", shapes)]
         _on(x8, *outs)
-    with _on(x8, x_scale, w8, w_scale, bias, workspace):
+    new = out is None
+    with _on(x8, x_scale, w8, w_scale, bias, workspace, stream=stream):
         if out is None:
             u = x8.new_empty(shapes[0], dtype=_BF16)
             v = x8.new_empty(shapes[1], dtype=_BF16)
@@ -583,6 +607,8 @@ def hstu_uvqk_fp8_fwd(x8, x_scale, w8, w_scale, num_heads: int, d_qk: int, d_v: 
                                    _stream_of(x8, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_uvqk_fp8_fwd")
+    if new:
+        _hand_over(stream, *out.values())
     return out
 
 
@@ -615,7 +641,8 @@ def hstu_rab_bucket_fwd(table, length: int, thresholds, *, out=None, stream=None
     length = int(length)
     if length < 1:
         raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_rab_bucket_fwd")
-    with _on(table, out):
+    new = out is None
+    with _on(table, out, stream=stream):
         if out is None:
             out = table.new_empty((H, 2 * length - 1))
             op = out.data_ptr()
@@ -624,6 +651,7 @@ def hstu_rab_bucket_fwd(table, length: int, thresholds, *, out=None, stream=None
         rc = lib.hstu_rab_bucket_fwd(H, length, NB, thr, tp, op, _stream_of(table, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rab_bucket_fwd")
+    _hand_over(stream, out if new else None)
     return out
 
 
@@ -637,13 +665,15 @@ def hstu_rab_bucket_bwd(d_rab_pos, num_buckets: int, thresholds, *, out=None, st
         raise ValueError("d_rab_pos must be [H, 2L - 1]")
     NB = int(num_buckets)
     thr = _thresholds(thresholds, NB)
-    with _on(d_rab_pos, out):
+    new = out is None
+    with _on(d_rab_pos, out, stream=stream):
         if out is None:
             out = d_rab_pos.new_empty((H, NB))
         rc = lib.hstu_rab_bucket_bwd(H, (W + 1) // 2, NB, thr, gp, _arg(out, "out", _F32, H, NB),
                                      _stream_of(d_rab_pos, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_rab_bucket_bwd")
+    _hand_over(stream, out if new else None)
     return out
 
 
@@ -674,7 +704,8 @@ def hstu_kv4_pack(k, v, *, cache=None, rows=None, workspace=None, stream=None):
     T, H = k.shape[0], k.shape[1]
     kp, vp = _arg(k, "k", _BF16, T, H, 128), _arg(v, "v", _BF16, T, H, 128)
     rp = _arg(rows, "rows", _I32, T)
-    with _on(k, v, rows, workspace, *(cache or ())):
+    new = cache is None
+    with _on(k, v, rows, workspace, *(cache or ()), stream=stream):
         if cache is None:
             if rows is not None:
                 raise ValueError("rows need a cache")
@@ -689,6 +720,8 @@ def hstu_kv4_pack(k, v, *, cache=None, rows=None, workspace=None, stream=None):
         rc = lib.hstu_kv4_pack(T, H, kp, vp, rp, R, *ptrs, wp, wn, _stream_of(k, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_kv4_pack")
+    if new:
+        _hand_over(stream, *cache)
     return cache
 
 
@@ -700,10 +733,11 @@ def hstu_kv4_unpack(cache, *, rows=None, out=None, workspace=None, stream=None):
     rp = _arg(rows, "rows", _I32)
     T = R if rows is None else rows.numel()
     ref = cache[0]
-    with _on(ref, *cache, rows, workspace, *(out or ())):
+    new = out is None
+    with _on(ref, *cache, rows, workspace, *(out or ()), stream=stream):
         if out is None:
-            new = ref.new_empty if rows is None else ref.new_zeros
-            out = new((T, H, 128), dtype=_BF16), new((T, H, 128), dtype=_BF16)
+            make = ref.new_empty if rows is None else ref.new_zeros
+            out = make((T, H, 128), dtype=_BF16), make((T, H, 128), dtype=_BF16)
         k, v = out
         kp, vp = _arg(k, "k", _BF16, T, H, 128), _arg(v, "v", _BF16, T, H, 128)
         wp, wn = None, 0
@@ -712,6 +746,8 @@ def hstu_kv4_unpack(cache, *, rows=None, out=None, workspace=None, stream=None):
         rc = lib.hstu_kv4_unpack(T, H, *ptrs, rp, R, kp, vp, wp, wn, _stream_of(ref, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_kv4_unpack")
+    if new:
+        _hand_over(stream, k, v)
     return k, v
 
 
@@ -761,8 +797,9 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
         total_tokens = limit
     elif timestamps is not None and total_tokens > limit:
         raise ValueError("total_tokens exceeds the timestamps' length")
+    new = y is None
     with _on(q, *cache, offsets, k, v, u, cand_offsets, first_rows, timestamps, cand_timestamps,
-             rab_pos, rab_time, ln_weight, ln_bias, y, workspace):
+             rab_pos, rab_time, ln_weight, ln_bias, y, workspace, stream=stream):
         p = hstu_problem_t(HSTU_BF16, B, int(total_tokens), max_seq_len, H, 128, 128,
                            _arg(offsets, "offsets", _I32, B + 1),
                            None if offsets_host is None else offsets_host.data_ptr(),
@@ -787,4 +824,5 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
             _stream_of(q, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_cand_kv4_fwd")
+    _hand_over(stream, y if new else None)
     return y
