@@ -219,23 +219,26 @@ def hstu_attn_fwd(q, k, v, u, offsets, max_seq_len, *, timestamps=None, rab_pos=
     D = H * v.shape[-1]
     p = make_problem(q, v, offsets, max_seq_len, timestamps, rab_pos, rab_time, norm_len, eps,
                      offsets_host, ln_weight, ln_bias)
-    if y is None:
-        y = torch.empty((T, D), dtype=q.dtype, device=q.device)
-    _dev(y, "y", q.dtype)
-    if save_for_backward and saved is None:
-        saved = (torch.empty((T, D), dtype=torch.float32, device=q.device),
-                 torch.empty((T,), dtype=torch.float32, device=q.device),
-                 torch.empty((T,), dtype=torch.float32, device=q.device))
-    if not save_for_backward:
-        saved = None
-    if workspace is None:
-        workspace = new_workspace(p, False, q.device)
-    o_save, mean, rstd = saved if saved is not None else (None, None, None)
-    rc = lib.hstu_attn_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(u), _ptr(y),
-                           _ptr(o_save), _ptr(mean), _ptr(rstd), _ptr(workspace),
-                           workspace.numel(), _stream_ptr(stream))
+    new_y, new_saved = y is None, save_for_backward and saved is None
+    with _on(q, stream=stream):
+        if y is None:
+            y = torch.empty((T, D), dtype=q.dtype, device=q.device)
+        _dev(y, "y", q.dtype)
+        if save_for_backward and saved is None:
+            saved = (torch.empty((T, D), dtype=torch.float32, device=q.device),
+                     torch.empty((T,), dtype=torch.float32, device=q.device),
+                     torch.empty((T,), dtype=torch.float32, device=q.device))
+        if not save_for_backward:
+            saved = None
+        if workspace is None:
+            workspace = new_workspace(p, False, q.device)
+        o_save, mean, rstd = saved if saved is not None else (None, None, None)
+        rc = lib.hstu_attn_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(u), _ptr(y),
+                               _ptr(o_save), _ptr(mean), _ptr(rstd), _ptr(workspace),
+                               workspace.numel(), _stream_of(q, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_attn_fwd")
+    _hand_over(stream, y if new_y else None, *(saved if new_saved else ()))
     return y, saved
 
 
@@ -256,29 +259,33 @@ def hstu_attn_bwd(dy, q, k, v, u, offsets, max_seq_len, saved, *, timestamps=Non
     _dev(ln_bias, "ln_bias", torch.float32)
     p = make_problem(q, v, offsets, max_seq_len, timestamps, rab_pos, rab_time, norm_len, eps,
                      offsets_host, ln_weight, ln_bias)
-    if grads is None:
-        grads = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-                     du=torch.empty_like(u),
-                     d_rab_pos=(torch.empty_like(rab_pos)
-                                if (rab_pos is not None and need_rab_grads) else None),
-                     d_rab_time=(torch.empty_like(rab_time)
-                                 if (rab_time is not None and need_rab_grads) else None),
-                     d_ln_weight=(torch.empty_like(ln_weight)
-                                  if (ln_weight is not None and need_rab_grads) else None),
-                     d_ln_bias=(torch.empty_like(ln_bias)
-                                if (ln_bias is not None and need_rab_grads) else None))
-    grads.setdefault("d_ln_weight", None)
-    grads.setdefault("d_ln_bias", None)
-    if workspace is None:
-        workspace = new_workspace(p, True, q.device)
-    rc = lib.hstu_attn_bwd(ctypes.byref(p), _ptr(dy), _ptr(q), _ptr(k), _ptr(v), _ptr(u),
-                           _ptr(o_save), _ptr(mean), _ptr(rstd), _ptr(grads["dq"]),
-                           _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads["du"]),
-                           _ptr(grads["d_rab_pos"]), _ptr(grads["d_rab_time"]),
-                           _ptr(grads["d_ln_weight"]), _ptr(grads["d_ln_bias"]),
-                           _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    new = grads is None
+    with _on(q, stream=stream):
+        if grads is None:
+            grads = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                         du=torch.empty_like(u),
+                         d_rab_pos=(torch.empty_like(rab_pos)
+                                    if (rab_pos is not None and need_rab_grads) else None),
+                         d_rab_time=(torch.empty_like(rab_time)
+                                     if (rab_time is not None and need_rab_grads) else None),
+                         d_ln_weight=(torch.empty_like(ln_weight)
+                                      if (ln_weight is not None and need_rab_grads) else None),
+                         d_ln_bias=(torch.empty_like(ln_bias)
+                                    if (ln_bias is not None and need_rab_grads) else None))
+        grads.setdefault("d_ln_weight", None)
+        grads.setdefault("d_ln_bias", None)
+        if workspace is None:
+            workspace = new_workspace(p, True, q.device)
+        rc = lib.hstu_attn_bwd(ctypes.byref(p), _ptr(dy), _ptr(q), _ptr(k), _ptr(v), _ptr(u),
+                               _ptr(o_save), _ptr(mean), _ptr(rstd), _ptr(grads["dq"]),
+                               _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads["du"]),
+                               _ptr(grads["d_rab_pos"]), _ptr(grads["d_rab_time"]),
+                               _ptr(grads["d_ln_weight"]), _ptr(grads["d_ln_bias"]),
+                               _ptr(workspace), workspace.numel(), _stream_of(q, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_attn_bwd")
+    if new:
+        _hand_over(stream, *grads.values())
     return grads
 
 
@@ -318,21 +325,25 @@ def hstu_uvqk_fwd(x, w, num_heads: int, d_qk: int, d_v: int, *, bias=None, act: 
     _dev(bias, "bias", torch.float32)
     T, E = x.shape
     H = int(num_heads)
-    if out is None:
-        out = dict(u=torch.empty((T, H * d_v), dtype=x.dtype, device=x.device),
-                   v=torch.empty((T, H, d_v), dtype=x.dtype, device=x.device),
-                   q=torch.empty((T, H, d_qk), dtype=x.dtype, device=x.device),
-                   k=torch.empty((T, H, d_qk), dtype=x.dtype, device=x.device))
-    for n in ("u", "v", "q", "k"):
-        _dev(out[n], n, x.dtype)
-    if workspace is None:
-        workspace = _status_workspace(x.device)
-    rc = lib.hstu_uvqk_fwd(int(T), int(E), H, int(d_qk), int(d_v), int(act), _ptr(x), _ptr(w),
-                           _ptr(bias), _ptr(out["u"]), _ptr(out["v"]), _ptr(out["q"]),
-                           _ptr(out["k"]), _ptr(workspace), workspace.numel(),
-                           _stream_ptr(stream))
+    new = out is None
+    with _on(x, stream=stream):
+        if out is None:
+            out = dict(u=torch.empty((T, H * d_v), dtype=x.dtype, device=x.device),
+                       v=torch.empty((T, H, d_v), dtype=x.dtype, device=x.device),
+                       q=torch.empty((T, H, d_qk), dtype=x.dtype, device=x.device),
+                       k=torch.empty((T, H, d_qk), dtype=x.dtype, device=x.device))
+        for n in ("u", "v", "q", "k"):
+            _dev(out[n], n, x.dtype)
+        if workspace is None:
+            workspace = _status_workspace(x.device)
+        rc = lib.hstu_uvqk_fwd(int(T), int(E), H, int(d_qk), int(d_v), int(act), _ptr(x), _ptr(w),
+                               _ptr(bias), _ptr(out["u"]), _ptr(out["v"]), _ptr(out["q"]),
+                               _ptr(out["k"]), _ptr(workspace), workspace.numel(),
+                               _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_uvqk_fwd")
+    if new:
+        _hand_over(stream, *out.values())
     return out
 
 
@@ -348,21 +359,24 @@ def hstu_out_fwd(y, w, x, *, bias=None, ln_weight=None, ln_bias=None, eps: float
         _dev(t, n, torch.float32)
     T, D = y.shape
     E = x.shape[1]
-    if z is None:
-        z = torch.empty((T, E), dtype=x.dtype, device=x.device)
-    _dev(z, "z", x.dtype)
-    stats = None
-    if save_stats:
-        stats = (torch.empty(T, dtype=torch.float32, device=x.device),
-                 torch.empty(T, dtype=torch.float32, device=x.device))
-    if workspace is None:
-        workspace = _status_workspace(x.device)
-    mean, rstd = stats if stats is not None else (None, None)
-    rc = lib.hstu_out_fwd(int(T), int(E), int(D), _ptr(y), _ptr(w), _ptr(x), _ptr(bias),
-                          _ptr(ln_weight), _ptr(ln_bias), float(eps), _ptr(z), _ptr(mean),
-                          _ptr(rstd), _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    new = z is None
+    with _on(x, stream=stream):
+        if z is None:
+            z = torch.empty((T, E), dtype=x.dtype, device=x.device)
+        _dev(z, "z", x.dtype)
+        stats = None
+        if save_stats:
+            stats = (torch.empty(T, dtype=torch.float32, device=x.device),
+                     torch.empty(T, dtype=torch.float32, device=x.device))
+        if workspace is None:
+            workspace = _status_workspace(x.device)
+        mean, rstd = stats if stats is not None else (None, None)
+        rc = lib.hstu_out_fwd(int(T), int(E), int(D), _ptr(y), _ptr(w), _ptr(x), _ptr(bias),
+                              _ptr(ln_weight), _ptr(ln_bias), float(eps), _ptr(z), _ptr(mean),
+                              _ptr(rstd), _ptr(workspace), workspace.numel(), _stream_of(x, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_out_fwd")
+    _hand_over(stream, z if new else None, *(stats or ()))
     return z, stats
 
 
@@ -388,20 +402,23 @@ def hstu_cand_fwd(k_hist, v_hist, offsets, max_seq_len, q, k, v, u, cand_offsets
     p = make_problem(k_hist, v_hist, offsets, max_seq_len, timestamps, rab_pos, rab_time,
                      norm_len, eps, offsets_host, ln_weight, ln_bias)
     C, H, _ = q.shape
-    if y is None:
-        y = torch.empty((C, H * v.shape[-1]), dtype=q.dtype, device=q.device)
-    _dev(y, "y", q.dtype)
-    if workspace is None:
-        n = int(lib.hstu_cand_workspace_size(ctypes.byref(p), int(C), int(max_cands)))
-        if n == 0:
-            raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_cand_workspace_size")
-        workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
-    rc = lib.hstu_cand_fwd(ctypes.byref(p), _ptr(k_hist), _ptr(v_hist), _ptr(cand_offsets),
-                           int(C), int(max_cands), _ptr(cand_timestamps), _ptr(q), _ptr(k),
-                           _ptr(v), _ptr(u), _ptr(y), _ptr(workspace), workspace.numel(),
-                           _stream_ptr(stream))
+    new = y is None
+    with _on(q, stream=stream):
+        if y is None:
+            y = torch.empty((C, H * v.shape[-1]), dtype=q.dtype, device=q.device)
+        _dev(y, "y", q.dtype)
+        if workspace is None:
+            n = int(lib.hstu_cand_workspace_size(ctypes.byref(p), int(C), int(max_cands)))
+            if n == 0:
+                raise HSTUError(HSTU_ERR_INVALID_ARG, "hstu_cand_workspace_size")
+            workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
+        rc = lib.hstu_cand_fwd(ctypes.byref(p), _ptr(k_hist), _ptr(v_hist), _ptr(cand_offsets),
+                               int(C), int(max_cands), _ptr(cand_timestamps), _ptr(q), _ptr(k),
+                               _ptr(v), _ptr(u), _ptr(y), _ptr(workspace), workspace.numel(),
+                               _stream_of(q, stream))
     if rc != HSTU_OK:
         raise HSTUError(rc, "hstu_cand_fwd")
+    _hand_over(stream, y if new else None)
     return y
 
 

@@ -153,3 +153,108 @@ def test_outputs_given():
     torch.cuda.current_stream().wait_stream(s)
     assert got[0].data_ptr() == dx.data_ptr()
     same(got, want)
+
+
+def attention():
+    """Forward and backward inputs: position and time bias, affine LayerNorm."""
+    T, H = 1800, 4
+    q, k = rnd(1, T, H, 128, std=128 ** -0.5), rnd(2, T, H, 128, std=128 ** -0.5)
+    v, u, dy = rnd(3, T, H, 128), rnd(4, T, H * 128), rnd(5, T, H * 128)
+    kw = dict(timestamps=1_700_000_000 + 200 * torch.arange(T, device=DEV),
+              rab_pos=rnd(6, H, 1999, dtype=F32), rab_time=rnd(7, H, 128, dtype=F32),
+              ln_weight=1 + 0.1 * rnd(8, H * 128, dtype=F32), ln_bias=0.1 * rnd(9, H * 128, dtype=F32))
+    return (q, k, v, u, i32([0, 1000, 1800]), 1000), dy, kw
+
+
+def attn_forward():
+    args, _, kws = attention()
+
+    def call(**kw):
+        y, saved = pa.hstu_attn_fwd(*args, save_for_backward=True, **kws, **kw)
+        return [y, *saved]
+    return call
+
+
+def attn_backward():
+    args, dy, kws = attention()
+    _, saved = pa.hstu_attn_fwd(*args, save_for_backward=True, **kws)
+    # (the tables' gradients are sums by atomics, whose last bits vary)
+    return lambda **kw: [pa.hstu_attn_bwd(dy, *args, saved, **kws, **kw)[n]
+                         for n in ("dq", "dk", "dv", "du")]
+
+
+def uvqk():
+    x, w = rnd(1, 1000, 512), rnd(2, 2048, 512, std=512 ** -0.5)
+    return lambda **kw: list(pa.hstu_uvqk_fwd(x, w, 4, 128, 128, act=1, **kw).values())
+
+
+def out_projection():
+    y, w, x = rnd(1, 1000, 512), rnd(2, 512, 512, std=512 ** -0.5), rnd(3, 1000, 512)
+
+    def call(**kw):
+        z, stats = pa.hstu_out_fwd(y, w, x, save_stats=True, **kw)
+        return [z, *stats]
+    return call
+
+
+def cand_forward():
+    (k, v, _, _, off, n), _, kws = attention()
+    kws.pop("ln_weight"), kws.pop("ln_bias")
+    q, kc = rnd(11, 300, 4, 128, std=128 ** -0.5), rnd(12, 300, 4, 128, std=128 ** -0.5)
+    vc, uc = rnd(13, 300, 4, 128), rnd(14, 300, 512)
+    cts = kws["timestamps"][-1] + 500 * torch.arange(300, device=DEV)
+    kws["rab_pos"] = rnd(15, 4, 2 * n + 1, dtype=F32)
+    coff = i32([0, 140, 300])
+    return lambda **kw: [pa.hstu_cand_fwd(k, v, off, n, q, kc, vc, uc, coff, 160,
+                                          cand_timestamps=cts, **kws, **kw)]
+
+
+ATTENTION = dict(attn_forward=attn_forward, attn_backward=attn_backward, uvqk=uvqk,
+                 out_projection=out_projection, cand_forward=cand_forward)
+
+
+@pytest.mark.parametrize("name", list(ATTENTION))
+def test_temporaries_of_the_attention_belong_to_the_given_stream(name):
+    behind_and_before(ATTENTION[name]())
+
+
+class Watched:
+    """The library, noting where the workspaces of its calls are."""
+
+    def __init__(self, lib):
+        self.lib, self.rooms = lib, []
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+        if not name.startswith("hstu_") or name.endswith("_size"):
+            return f
+
+        def call(*args):      # .., workspace, its bytes, stream
+            at = getattr(args[-3], "value", args[-3])
+            if at:
+                self.rooms.append((int(at), int(args[-2])))
+            return f(*args)
+        return call
+
+
+@pytest.mark.parametrize("name", ["norm_backward", "uvqk_fp8", "unpack_rows", "scoring_few",
+                                  "scoring_many", "attn_forward", "attn_backward"])
+def test_workspaces_are_not_handed_out_early(name, monkeypatch):
+    """While the given stream is busy, the caller's allocations take none of the
+    memory that the call's workspace has."""
+    call = (CALLS.get(name) or ATTENTION[name])()
+    call()
+    lib = Watched(pa.load_library())
+    monkeypatch.setattr(pa._binding, "load_library", lambda: lib)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(LONG)
+    got = call(stream=s)
+    assert lib.rooms
+    at, n = lib.rooms[0]
+    mine = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(8)] + scribble()
+    for t in mine:
+        assert t.data_ptr() + t.numel() <= at or at + n <= t.data_ptr()
+    torch.cuda.synchronize()
+    del got
