@@ -811,7 +811,8 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
         total_tokens = int(offsets_host[-1])
     max_seq_len, max_cands = int(max_seq_len), int(max_cands)
     if total_tokens is None:
-        total_tokens = limit if B > 0 else 0
+        # (no users, or a cache without rows: no history either)
+        total_tokens = limit if B > 0 and R > 0 else 0
     elif timestamps is not None and total_tokens > limit:
         raise ValueError("total_tokens exceeds the timestamps' length")
     new = y is None

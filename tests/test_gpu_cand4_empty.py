@@ -35,3 +35,22 @@ def test_no_users(slots, time):
     y = pa.hstu_cand_kv4_fwd(cache, i32([0]), 40, *candidates(0), i32([0]), 0,
                              first_rows=i32([]) if slots else None, **kw)
     assert y.shape == (0, H * 128)
+
+
+@pytest.mark.parametrize("slots", [False, True])
+@pytest.mark.parametrize("cands", [[2, 0, 3], [30, 0, 20]])
+def test_a_cache_without_rows(cands, slots):
+    """Users that are all new: each candidate sees itself alone, as against a
+    cache that has rows; a history in such a cache is reported."""
+    C = sum(cands)
+    coff = i32([0, cands[0], cands[0], C])
+    rab = torch.randn(H, 21, generator=torch.Generator().manual_seed(9)).to(DEV)
+    kw = dict(first_rows=i32([0, 0, 0]) if slots else None, rab_pos=rab)
+    full = pa.hstu_kv4_pack(rnd(1, 8, H, 128), rnd(2, 8, H, 128))
+    args = (*candidates(C), coff, max(cands))
+    want = pa.hstu_cand_kv4_fwd(full, i32([0, 0, 0, 0]), 10, *args, **kw)
+    empty = pa.hstu_kv4_cache(0, H, DEV)
+    assert torch.equal(pa.hstu_cand_kv4_fwd(empty, i32([0, 0, 0, 0]), 10, *args, **kw), want)
+    ws = pa.hstu_cand_kv4_workspace(3, H, 10, C, max(cands), DEV)
+    pa.hstu_cand_kv4_fwd(empty, i32([0, 5, 5, 5]), 10, *args, workspace=ws, **kw)
+    assert pa.hstu_attn_check(ws) == pa._binding.HSTU_ERR_INVALID_ARG
