@@ -787,8 +787,10 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
     """hstu_cand_fwd against histories in a 4-bit cache (hstu_kv4_pack): user b's
     history is the cache rows first_rows[b].. (int32 [B]), or, without
     first_rows, the rows offsets[b]..offsets[b+1]-1.  total_tokens bounds
-    offsets[B] (default: the timestamps' length, else the cache's rows, or, with
-    first_rows, no bound).  Returns y [C, H*128]."""
+    offsets[B] (default: the timestamps' length and, without first_rows, the
+    cache's rows).  q, k, v, u may be longer than cand_offsets[B] and timestamps
+    than offsets[B]; rows of y that belong to no user stay as they were.  Returns
+    y [C, H*128]."""
     lib = load_library()
     R, HC, ptrs = _cache_args(cache)
     qp = _arg(q, "q", _BF16)
@@ -802,8 +804,7 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
         raise ValueError("timestamps must be [T]")
     W = 0 if rab_pos is None else rab_pos.shape[1]
     NB = 0 if rab_time is None else rab_time.shape[-1]
-    limit = (timestamps.numel() if timestamps is not None else
-             R if first_rows is None else 2 ** 31 - 1)
+    limit = timestamps.numel() if timestamps is not None else 2 ** 31 - 1
     if offsets_host is not None:
         if (offsets_host.is_cuda or offsets_host.dtype != _I32 or offsets_host.shape != (B + 1,)
                 or not offsets_host.is_contiguous()):
@@ -812,7 +813,7 @@ def hstu_cand_kv4_fwd(cache, offsets, max_seq_len: int, q, k, v, u, cand_offsets
     max_seq_len, max_cands = int(max_seq_len), int(max_cands)
     if total_tokens is None:
         # (no users, or a cache without rows: no history either)
-        total_tokens = limit if B > 0 and R > 0 else 0
+        total_tokens = (min(limit, R) if first_rows is None else limit) if B > 0 and R > 0 else 0
     elif timestamps is not None and total_tokens > limit:
         raise ValueError("total_tokens exceeds the timestamps' length")
     new = y is None

@@ -54,3 +54,14 @@ def test_a_cache_without_rows(cands, slots):
     ws = pa.hstu_cand_kv4_workspace(3, H, 10, C, max(cands), DEV)
     pa.hstu_cand_kv4_fwd(empty, i32([0, 5, 5, 5]), 10, *args, workspace=ws, **kw)
     assert pa.hstu_attn_check(ws) == pa._binding.HSTU_ERR_INVALID_ARG
+
+
+def test_timestamps_longer_than_the_cache():
+    """A timestamp buffer of a fixed size over a cache of the batch's rows."""
+    cache = pa.hstu_kv4_pack(rnd(1, 60, H, 128), rnd(2, 60, H, 128))
+    ts = 1_700_000_000 + 100 * torch.arange(200, device=DEV)
+    rab = torch.randn(H, 128, generator=torch.Generator().manual_seed(9)).to(DEV)
+    args = (cache, i32([0, 25, 60]), 40, *candidates(7), i32([0, 3, 7]), 4)
+    kw = dict(cand_timestamps=ts[60:67].clone(), rab_time=rab)
+    want = pa.hstu_cand_kv4_fwd(*args, timestamps=ts[:60].clone(), **kw)
+    assert torch.equal(pa.hstu_cand_kv4_fwd(*args, timestamps=ts, **kw), want)
