@@ -780,7 +780,7 @@ HSTU_API size_t hstu_rmsnorm_bwd_workspace_size(int32_t T, int32_t E) {
   if (T < 0 || T > kMaxT || E < 1 || E > kMaxE) return 0;
   // no less than smaller calls of any row length need
   size_t n = static_cast<size_t>(bwd_blocks(T, E)) * E * sizeof(float);
-  for (int e = 256; e < E; e *= 2) {
+  for (int e = 64; e < E; e *= 2) {
     const size_t m = static_cast<size_t>(bwd_blocks(T, e)) * e * sizeof(float);
     if (m > n) n = m;
   }
