@@ -311,8 +311,8 @@ HSTU_API hstu_status_t hstu_quant_rows(hstu_dtype_t dtype, int32_t T, int32_t E,
  * is the gradient that reaches h by the residual stream; dx may be d_residual
  * or dy.  d_weight fp32 [E] or NULL is overwritten, and added up in an order
  * that depends on the sizes alone.  With d_weight, workspace:
- * hstu_rmsnorm_bwd_workspace_size bytes, 256-byte aligned, any contents (it
- * holds no status word).
+ * hstu_rmsnorm_bwd_workspace_size bytes (which grow with T and E), 256-byte
+ * aligned, any contents (it holds no status word).
  */
 HSTU_API size_t hstu_rmsnorm_bwd_workspace_size(int32_t T, int32_t E);
 HSTU_API hstu_status_t hstu_rmsnorm_bwd(hstu_dtype_t dtype, int32_t T, int32_t E, const void *dy,
@@ -322,7 +322,10 @@ HSTU_API hstu_status_t hstu_rmsnorm_bwd(hstu_dtype_t dtype, int32_t T, int32_t E
 
 /*
  * UVQK projection of 8-bit rows: act((x8 w8^T) x_scale_t w_scale_n + bias_n),
- * split and laid out as by hstu_uvqk_fwd (bf16 outputs, rounded once).
+ * split and laid out as by hstu_uvqk_fwd (bf16 outputs, rounded once; with
+ * act = 1 SiLU is x/2 (1 + tanh(x/2)) with the hardware's tanh, which may add
+ * |x| 2^-12 by its documented bound; measured: |x| 2^-19, which leaves results
+ * bf16's digits down to x = -8).
  * x8 [T, E], w8 [N, E] e4m3; x_scale fp32 [T], w_scale fp32 [N]; all pointers
  * 16-byte aligned.  Supported: E a multiple of 16; H*d_v and H*d_qk multiples
  * of 256; T <= 8388480.  workspace: 256 bytes, as for hstu_uvqk_fwd.
@@ -400,6 +403,13 @@ HSTU_API hstu_status_t hstu_kv4_unpack(int32_t T, int32_t H, const void *k_codes
  * are packed as the tokens are, first row offsets[b], cache_rows >=
  * total_tokens).  Users may share rows.  timestamps stay packed by offsets.
  * p->total_tokens need only bound offsets[B] (and the timestamps' length).
+ * total_cands is the length of q .. y, which may be more than the users' own
+ * candidates cand_offsets[0] .. cand_offsets[B] - 1: y's other rows are not
+ * written, and the sums take no room for them.
+ * Attention weights enter the sums in two bf16 parts where max_cands <= 16
+ * (2^-16 of a weight is lost); with more as one bf16 number, of the hardware's
+ * tanh, as in hstu_cand_fwd.  A candidate's score can so differ in its last bf16
+ * digits between a call of either kind.
  * Supported: bf16, d_qk = d_v = 128, 1 <= H <= 16.  Groups whose scale exceeds
  * 2^123 are not finite here.  workspace: hstu_cand_kv4_workspace_size bytes,
  * 256-byte aligned, zero-filled before its first use; beyond the status word

@@ -5,6 +5,10 @@ only checks tensor placement, builds the ``hstu_problem_t`` struct, allocates
 outputs and workspace with torch (device memory is plumbing) and forwards
 raw pointers.  There is no fallback: if libhstu.so is missing, or a tensor is
 not on a CUDA device, the call raises.
+
+``stream=`` takes a torch.cuda.Stream: the call runs on it, and what it
+allocates or clears belongs to it.  The inputs have to be ready there; the
+caller's stream waits for it before it reads the outputs.
 """
 from __future__ import annotations
 

@@ -33,10 +33,11 @@
 // the LayerNorm and the gate.
 //
 // Measured on a B200: one candidate for each of 32 users, 8 heads, histories of
-// 256-4096 tokens (81 MB of cache): 46 us (the bytes alone take 12).  Issue
-// slots bound it, half busy with 16 warps an SM: some 500 instructions per 16
-// keys and head, of which decoding takes 200, with 19 us of starts and the last
-// kernel (a user's 16 keys).  A CTA per (user, run of keys) left SMs idle at the
+// 256-4096 tokens (81 MB of cache): 46 us (the bytes alone take 12).  Latency
+// bounds it: a warp's chain of decoding, MMA, SiLU, transpose and MMA, some 500
+// instructions per 16 keys and head (200 of them decoding), leaves half of the
+// issue slots empty at 14 warps an SM; 19 us are starts and the last kernel (a
+// user's 16 keys).  A CTA per (user, run of keys) left SMs idle at the
 // end (64 us); cp.async by the lanes cost 145 shared-memory wavefronts a block.
 #include <cuda_bf16.h>
 
@@ -664,7 +665,8 @@ __global__ void __launch_bounds__(256) hstu_cand4_finish_rows(const __grid_const
   }
   const float inv_n = 1.0f / static_cast<float>(a.norm_len > 0 ? a.norm_len : us.nb + 1);
   const int slices = (us.nb + cut.chunk - 1) / cut.chunk;
-  const size_t sum0 = static_cast<size_t>(us.c0 - cfirst + i);
+  const size_t stride = static_cast<size_t>(a.sum_rows) * D;
+  const size_t sum0 = static_cast<size_t>(us.c0 - cfirst + i) * D + 4 * lane;
   uint2 v[NH];
 #pragma unroll
   for (int h = 0; h < NH; ++h) v[h] = row2(a.v, h);
@@ -673,8 +675,7 @@ __global__ void __launch_bounds__(256) hstu_cand4_finish_rows(const __grid_const
 #pragma unroll
   for (int h = 0; h < NH; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = 0; s < slices; ++s) {
-    const float* src =
-        a.part + checked(a.status, static_cast<size_t>(s) * a.sum_rows + sum0, a.part_rows, BS_CAND4_SUM) * D + 4 * lane;
+    const float* src = a.part + checked(a.status, s * stride + sum0, a.part_rows * D, BS_CAND4_SUM);
     float4 f[NH];
 #pragma unroll
     for (int h = 0; h < NH; ++h)

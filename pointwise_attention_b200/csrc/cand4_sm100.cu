@@ -27,8 +27,9 @@
 // status word and the CTA leaves through the same barriers.
 //
 // Measured on a B200: 512 candidates for each of 32 users, 8 heads, histories of
-// 256-4096 tokens, position and time bias, 146 GFLOP: 311 us here, 380 us with the
-// plan pass (15) and the last kernel (59).  Latency bounds it: a key tile's chain of products, epilogue and
+// 256-4096 tokens, position and time bias, 146 GFLOP: 311 us here; with the plan
+// pass (15) and the last kernel (62), which start beside it, 357 to 385 us a call
+// by the lengths drawn.  Latency bounds it: a key tile's chain of products, epilogue and
 // barriers takes about 5300 cycles where the tensor core needs 2200 and tanh
 // 2048.  Half tiles with barriers of their own (64 keys) did not help: their
 // MMAs take as long to issue as whole ones.
