@@ -258,3 +258,33 @@ def test_workspaces_are_not_handed_out_early(name, monkeypatch):
         assert t.data_ptr() + t.numel() <= at or at + n <= t.data_ptr()
     torch.cuda.synchronize()
     del got
+
+
+def test_nothing_on_a_given_stream():
+    """Calls without rows allocate nothing to hand over."""
+    s, none = torch.cuda.Stream(), rnd(1, 0, 64)
+    assert pa.hstu_rmsnorm_fwd(none, quant=True, stream=s)["q8"].shape == (0, 64)
+    assert pa.hstu_quant_rows(none, stream=s)[0].shape == (0, 64)
+    dx, dw = pa.hstu_rmsnorm_bwd(none, none, rnd(2, 0, dtype=F32), stream=s)
+    s.synchronize()
+    assert dx.shape == (0, 64) and bool((dw == 0).all())
+    cache = pa.hstu_kv4_pack(none.view(0, 2, 128), none.view(0, 2, 128), stream=s)
+    assert pa.hstu_kv4_unpack(cache, stream=s)[0].shape == (0, 2, 128)
+
+
+def test_a_stream_that_is_captured():
+    """A call given the stream of a capture: its outputs and workspace belong to
+    the graph, and replays follow the inputs."""
+    call = norm_backward()
+    want = [t.clone() for t in call()]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = call(stream=s)
+    junk = scribble()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    same(got, want)
+    del junk
