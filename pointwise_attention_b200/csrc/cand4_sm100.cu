@@ -28,7 +28,7 @@
 //
 // Measured on a B200: 512 candidates for each of 32 users, 8 heads, histories of
 // 256-4096 tokens, position and time bias, 146 GFLOP: 311 us here; with the plan
-// pass (15) and the last kernel (62), which start beside it, 357 to 385 us a call
+// pass (15) and the last kernel (62), which start beside it, 332 to 385 us a call
 // by the lengths drawn.  Latency bounds it: a key tile's chain of products, epilogue and
 // barriers takes about 5300 cycles where the tensor core needs 2200 and tanh
 // 2048.  Half tiles with barriers of their own (64 keys) did not help: their
